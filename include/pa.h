@@ -70,6 +70,7 @@ enum {
 #define PA_DEVERR_BAD_PAIR    0x8u  /* copy_blocks / swap_blocks: a block id outside its pool */
 #define PA_DEVERR_TIMEOUT     0x10u /* a bounded wait gave up (about 1 s; prefill pipeline, decode
                                          split-KV merge): output invalid */
+#define PA_DEVERR_NO_BLOCKS   0x20u /* build_step: fewer free blocks than the step needs */
 
 /*
  * pa_reshape_and_cache -- write each new token's K and V rows into its cache slot.
@@ -119,8 +120,9 @@ int pa_reshape_and_cache(const void* key, const void* value, void* k_cache, void
  * It reads context_lens and block_tables (to plan its work) while that kernel drains,
  * and q, the caches and the workspace only after it has finished.  So block_tables and
  * context_lens must not be written by the kernel immediately before it in the stream
- * when that kernel lets its dependents start early (no kernel of this library writes
- * them; a plain copy or a kernel without programmatic launch is always safe).  The same
+ * when that kernel lets its dependents start early (pa_build_step, the one kernel of this
+ * library that writes tables, lets none start early; a plain copy or a kernel without
+ * programmatic launch is always safe).  The same
  * holds for every decode entry point below.
  */
 int pa_decode(const void* q, const void* k_cache, const void* v_cache,
@@ -228,6 +230,108 @@ int pa_swap_blocks_int4(const void* src_k, const void* src_v, const float* src_k
                         float* dst_vs, const int32_t* block_mapping, int num_pairs,
                         int src_num_blocks, int dst_num_blocks, int num_kv_heads, int head_dim,
                         int block_size, cudaStream_t stream);
+
+/*
+ * pa_build_step -- block tables and slots of one step from request lengths, on the GPU.
+ *
+ * The host pool (pa_pool_*) plans blocks one request at a time.  This call plans a whole step
+ * where the lengths already are, so that decode steps can follow one another, or a captured
+ * graph replay, with no round trip to the host.  Request s has context_lens[s] tokens in this
+ * step, query_lens[s] of them new.  With old_s = ceil((c_s - q_s) / B) and need_s =
+ * ceil(c_s / B) - old_s (aiqz.cc, section 分页存储设计, N_i = ceil(S_i / B)), o_s the sum of
+ * need over the requests before s, and N_s the sum of their new tokens:
+ *   block_tables[s][old_s + k] = free_blocks[free_start[0] + o_s + k],   k < need_s
+ *   slot_mapping[N_s + i] = block_tables[s][p / B] * B + p % B,          p = c_s - q_s + i
+ *   query_start[s] = N_s,   query_start[num_seqs] = N,   free_next[0] = free_start[0] + sum need
+ * Blocks leave the head of the list in request order, as from the host pool's free list.
+ * slot_mapping entries N .. num_slots - 1 are -1 (a padded batch: the cache writes skip
+ * them).  Other table entries are left as they were; the old_s entries of a request are read.
+ * A request may have no new tokens (q_s = 0) and no context.  A tail block shared with
+ * another sequence must have been copied first (pa_copy_blocks*).
+ *
+ * Device: query_lens, context_lens [num_seqs], free_blocks [num_free], free_start [1],
+ * block_tables [num_seqs][max_blocks_per_seq], query_start [num_seqs + 1], free_next [1],
+ * all int32; slot_mapping [num_slots] int64.  free_next must not be free_start (a loop
+ * alternates two cells) and no output may overlap an input.
+ *
+ * A step that needs more blocks than free_blocks holds behind free_start[0]
+ * (PA_DEVERR_NO_BLOCKS; also a free_start[0] outside [0, num_free]), or more slots than
+ * num_slots (PA_DEVERR_BAD_SLOT), changes no table, sets every slot to -1 and free_next to
+ * free_start; query_start is written all the same (clipped to 2^31 - 1).  An impossible
+ * request (negative length, q_s > c_s, c_s > max_blocks_per_seq * B) gets no blocks, slots
+ * -1 for its max(q_s, 0) tokens, and PA_DEVERR_BAD_CONTEXT; a block id outside [0,
+ * num_blocks) gives slots -1 and PA_DEVERR_BAD_BLOCK, and is not written into a table.
+ * num_seqs == 0 writes query_start[0] = 0, free_next and the slots.
+ * The launch waits for the kernel before it and lets none after it start early, so the
+ * tables it writes may be read by any call that follows it in the stream.
+ */
+int pa_build_step(const int32_t* query_lens, const int32_t* context_lens, int num_seqs,
+                  const int32_t* free_blocks, int num_free, const int32_t* free_start,
+                  int32_t* block_tables, int max_blocks_per_seq, int block_size, int num_blocks,
+                  int64_t* slot_mapping, int num_slots, int32_t* query_start, int32_t* free_next,
+                  cudaStream_t stream);
+
+/*
+ * FP8 KV blocks with a scale for each (block, kv head).  The caches hold E4M3 codes as above,
+ *   k_cache, v_cache    [num_blocks][Hkv][B][d]
+ *   k_scales, v_scales  [num_blocks][Hkv] float32
+ * and a code c of kv head h in block b means decode(c) * scales[b][h].  Nothing has to be
+ * calibrated: the cache write chooses each scale from the data.  The scales it stores are
+ * powers of two 2^e, -100 <= e <= 120; a floating-point code loses nothing by that.  Other
+ * finite positive scales (a cache made elsewhere) are read as they are.  Codes 16-byte,
+ * scales 4-byte aligned, all owned by the caller.
+ */
+/* Cache write of each sequence's newest tokens.  Sequence s owns rows query_start[s] ..
+ * query_start[s+1]-1 of key / value [num_tokens][Hkv][d] (fp16 or bf16, `dtype`), its positions
+ * c - q .. c - 1 (c = context_lens[s], q = their number): one row for a decode step, a prompt
+ * or a chunk of one otherwise, mixed freely.  Rows from query_start[num_seqs] on (a padded
+ * batch) are not read.  For each block that these positions touch, kv head h, and K and V
+ * apart:
+ *   amax = the largest finite |x| of the new rows, e = the smallest integer with
+ *   amax <= 448 * 2^e, held in [-100, 120];  S = 2^e if the call writes the block's row 0,
+ *   else max(2^e, scales[b][h]);
+ *   earlier rows of the block, where S > scales[b][h]: code := E4M3(decode(code) *
+ *   scales[b][h] / S) (for powers of two exact, but where the result is subnormal);
+ *   new rows: code = E4M3(x / S), rounding to nearest-even, magnitudes above 448 S (only
+ *   infinities) clamped, NaN kept.  scales[b][h] = S.
+ * Rows of a touched block behind the last new one are left as they were.  A touched block
+ * must belong to one sequence of the call (copy-on-write first), and its rows before c - q
+ * must have been written by this call's kind.  A sequence with an impossible span
+ * (query_start decreasing or beyond num_tokens, q > c, c > max_blocks_per_seq * B) writes
+ * nothing: PA_DEVERR_BAD_CONTEXT; a block id out of range is skipped: PA_DEVERR_BAD_BLOCK.
+ * A launch is a programmatic dependent of the kernel before it; it reads everything only
+ * after that kernel has finished. */
+int pa_append_fp8_block(const void* key, const void* value, void* k_cache, void* v_cache,
+                        float* k_scales, float* v_scales, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* query_start, int num_seqs, int num_tokens, int num_blocks,
+                        int num_kv_heads, int head_dim, int block_size, pa_dtype dtype,
+                        cudaStream_t stream);
+/* pa_decode over those blocks: z_t = scale * sK_t * <q, decode(K codes_t)>, out = sum_t
+ * softmax(z)_t * sV_t * decode(V codes_t), sK_t and sV_t the scales of token t's block.  q and
+ * out are fp16 or bf16 (`dtype`).  The codes are widened to f16 exactly and multiplied on the
+ * tensor cores in f16 (bf16 queries rounded to f16, so |q| < 65520); the K scale multiplies
+ * the fp32 scores, the V scale the softmax weights before they are rounded to f16, relative
+ * to the largest V scale met so far, so that its size does not matter; accumulation fp32.
+ * Same workspace, ordering, error and determinism rules as pa_decode. */
+int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                        int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                        int num_blocks, float scale, void* out, void* workspace,
+                        size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream);
+/* pa_copy_blocks for those blocks: codes and scales of each pair, in one launch. */
+int pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                             const int32_t* block_mapping, int num_pairs, int num_blocks,
+                             int num_kv_heads, int head_dim, int block_size,
+                             cudaStream_t stream);
+/* pa_swap_blocks for those blocks: codes and scales move together between two pools (one of
+ * them may be pinned host memory), in one launch; the same pair rules. */
+int pa_swap_blocks_fp8_block(const void* src_k, const void* src_v, const float* src_ks,
+                             const float* src_vs, void* dst_k, void* dst_v, float* dst_ks,
+                             float* dst_vs, const int32_t* block_mapping, int num_pairs,
+                             int src_num_blocks, int dst_num_blocks, int num_kv_heads,
+                             int head_dim, int block_size, cudaStream_t stream);
 
 /*
  * pa_prefill -- causal multi-query attention of each sequence's newest tokens over its

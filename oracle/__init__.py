@@ -28,6 +28,8 @@ Modules:
     fp8         -- FP8 (E4M3) KV blocks: the format, the quantising cache write, decode.
     int4        -- INT4 KV blocks (codes with one scale per row): the format, the
                    quantising cache write, decode.
+    fp8_block   -- FP8 blocks with one scale per (block, kv head): the cache write, decode,
+                   prefill; and a step's block tables and slots from request lengths.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against something other than
 itself: values the pages print, closed forms, library special cases (NumPy float16,

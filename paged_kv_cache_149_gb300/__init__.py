@@ -37,6 +37,7 @@ DEVERR_BAD_CONTEXT = 0x2
 DEVERR_BAD_SLOT = 0x4
 DEVERR_BAD_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_NO_BLOCKS = 0x20
 
 PA_FP16 = 0
 PA_BF16 = 1
@@ -69,6 +70,16 @@ SIGNATURES = {
     "pa_copy_blocks_int4": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp]),
     "pa_swap_blocks_int4": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _vp]),
+    "pa_build_step": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i32,
+                             _vp, _vp, _vp]),
+    "pa_append_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
+                                   _i32, _i32, _i32, _i32, _i32, _vp]),
+    "pa_decode_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                                   _i32, _i32, _i32, _f32, _vp, _vp, _sz, _i32, _vp]),
+    "pa_copy_blocks_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                        _vp]),
+    "pa_swap_blocks_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
+                                        _i32, _i32, _i32, _i32, _vp]),
     "pa_prefill": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                           _i32, _i32, _f32, _vp, _i32, _vp]),
     "pa_decode_workspace_size": (_sz, [_i32, _i32, _i32]),
@@ -207,8 +218,8 @@ def _pool_device(src, dst, *args, device=None, **kw):
 
 class Launch:
     """A library call whose arguments were checked and marshalled once (``plan=True`` on
-    the decode step functions, prefill and reshape_and_cache): ``run(stream)`` issues it
-    again on ``stream`` over the
+    the decode step functions, decode_fp8_block, the prefills, reshape_and_cache,
+    append_fp8_block and build_step): ``run(stream)`` issues it again on ``stream`` over the
     same buffers, whose contents may change between runs.  For serving loops that launch
     the same step shape many times; the per-call cost is one foreign call.  The marshalled
     arguments are raw device addresses, so the Launch holds a reference to every tensor
@@ -682,6 +693,158 @@ def swap_blocks_int4(src, dst, block_mapping, stream=None, device=None):
         _reachable(block_mapping, "block_mapping", torch.int32), block_mapping.shape[0], nbs, nbd,
         hkv, 2 * d2, bs, _stream_ptr(stream, device))
     _check(st, "pa_swap_blocks_int4")
+
+
+@_on_first
+def build_step(query_lens, context_lens, free_blocks, free_start, block_tables, block_size,
+               num_blocks, slot_mapping, query_start=None, free_next=None, stream=None, plan=False):
+    """Block tables and slots of one step from request lengths, on the GPU: request s has
+    context_lens[s] tokens, query_lens[s] of them new.  Its missing blocks come from
+    free_blocks[free_start[0]:] in request order and are written into block_tables;
+    slot_mapping gets the slot of every new token (-1 past the last one); returns
+    (query_start [num_seqs + 1], free_next [1]).  A step that lacks blocks or slots changes
+    no table, sets every slot to -1 and a device error bit.  plan=True returns a Launch whose
+    runs return query_start (free_next must then be given)."""
+    import torch
+    n = query_lens.shape[0]
+    _need(query_lens.dim() == 1 and context_lens.shape == (n,), "query_lens and context_lens must be [num_seqs]")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    _need(free_blocks.dim() == 1 and slot_mapping.dim() == 1, "free_blocks and slot_mapping must be 1-D")
+    _need(free_start.numel() == 1, "free_start must hold one value")
+    if query_start is None or free_next is None:
+        _need(not plan, "a planned build_step needs query_start and free_next")
+        with torch.cuda.stream(stream):  # (allocated for the stream that writes them)
+            if query_start is None:
+                query_start = torch.empty(n + 1, dtype=torch.int32, device=query_lens.device)
+            if free_next is None:
+                free_next = torch.empty(1, dtype=torch.int32, device=query_lens.device)
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    _need(free_next.numel() == 1, "free_next must hold one value")
+    i32 = torch.int32
+    args = (_dev(query_lens, "query_lens", i32), _dev(context_lens, "context_lens", i32), n,
+            _dev(free_blocks, "free_blocks", i32), free_blocks.shape[0],
+            _dev(free_start, "free_start", i32), _dev(block_tables, "block_tables", i32),
+            block_tables.shape[1], int(block_size), int(num_blocks),
+            _dev(slot_mapping, "slot_mapping", torch.int64), slot_mapping.shape[0],
+            _dev(query_start, "query_start", i32), _dev(free_next, "free_next", i32))
+    if plan:
+        return Launch("pa_build_step", args, query_start,
+                      keep=(query_lens, context_lens, free_blocks, free_start, block_tables,
+                            slot_mapping, free_next))
+    _check(lib().pa_build_step(*args, _stream_ptr(stream, query_lens.device)), "pa_build_step")
+    return query_start, free_next
+
+
+def _fp8_block_cache(codes, scales, name):
+    """(codes, scales) addresses of one cache of FP8 blocks with block scales."""
+    import torch
+    if not (codes.dim() == 4 and scales.shape == codes.shape[:2]):
+        raise ValueError(f"{name}: codes [NB, Hkv, B, d] and scales [NB, Hkv]")
+    return _fp8_cache(codes, name + "_cache"), _dev(scales, name + "_scales", torch.float32)
+
+
+@_on_first
+def append_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                     query_start, stream=None, plan=False):
+    """Cache write of FP8 blocks with a scale per (block, kv head): sequence s's rows
+    query_start[s] .. query_start[s+1]-1 of key / value become its positions context_lens[s] -
+    q_len .. context_lens[s] - 1.  A block's scale is the smallest power of two that holds
+    its rows; where a new row raises it, the block's earlier rows are requantised.  Rows
+    behind the last sequence are not read.  plan=True returns a Launch instead of writing."""
+    import torch
+    ntok, hkv, d = key.shape
+    nb, hkv2, bs, d2 = k_cache.shape
+    n = context_lens.shape[0]
+    _need(value.shape == key.shape and v_cache.shape == k_cache.shape, "shape mismatch")
+    _need(hkv == hkv2 and d == d2, "shape mismatch")
+    _need(key.dtype == value.dtype, "dtype mismatch")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
+    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
+    args = (_dev(key, "key"), _dev(value, "value"), kc, vc, ks, vs,
+            _dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+            _dev(context_lens, "context_lens", torch.int32),
+            _dev(query_start, "query_start", torch.int32), n, ntok, nb, hkv, d, bs,
+            _dtype_code(key))
+    if plan:
+        return Launch("pa_append_fp8_block", args, k_cache,
+                      keep=(key, value, v_cache, k_scales, v_scales, block_tables, context_lens,
+                            query_start))
+    _check(lib().pa_append_fp8_block(*args, _stream_ptr(stream, key.device)), "pa_append_fp8_block")
+
+
+@_on_first
+def decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
+                     out=None, workspace=None, stream=None, plan=False):
+    """Paged decode over FP8 blocks with a scale per (block, kv head) (codes [NB, Hkv, B, d],
+    scales [NB, Hkv] float32); q and out are fp16 or bf16.  plan=True returns a Launch
+    instead of launching."""
+    import torch
+    n, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    _need(v_cache.shape == k_cache.shape and d == d2, "shape mismatch")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    _need(context_lens.shape == (n,), "context_lens must be [num_seqs]")
+    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
+    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    if workspace is None:
+        workspace = _scratch(hq, hkv, d, q.device, stream)
+    args = (_dev(q, "q"), kc, vc, ks, vs, _dev(block_tables, "block_tables", torch.int32),
+            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), n, hq, hkv, d,
+            bs, nb, float(scale), _dev(out, "out"), _dev(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _dtype_code(q))
+    if plan:
+        return Launch("pa_decode_fp8_block", args, out,
+                      keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                            workspace))
+    _check(lib().pa_decode_fp8_block(*args, _stream_ptr(stream, q.device)), "pa_decode_fp8_block")
+    return out
+
+
+@_on_first
+def copy_blocks_fp8_block(k_cache, v_cache, k_scales, v_scales, block_mapping, stream=None):
+    """copy_blocks for FP8 blocks with block scales: codes and scales of each (src, dst) pair
+    in one launch."""
+    import torch
+    nb, hkv, bs, d = k_cache.shape
+    _need(v_cache.shape == k_cache.shape, "shape mismatch")
+    _need(block_mapping.dim() == 2 and block_mapping.shape[1] == 2, "block_mapping must be [n, 2]")
+    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
+    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
+    st = lib().pa_copy_blocks_fp8_block(
+        kc, vc, ks, vs, _dev(block_mapping, "block_mapping", torch.int32), block_mapping.shape[0],
+        nb, hkv, d, bs, _stream_ptr(stream, k_cache.device))
+    _check(st, "pa_copy_blocks_fp8_block")
+
+
+@_runs_on(_pool_device)
+def swap_blocks_fp8_block(src, dst, block_mapping, stream=None, device=None):
+    """swap_blocks for FP8 blocks with block scales; src and dst are (k_cache, v_cache,
+    k_scales, v_scales) pools, CUDA tensors or pinned CPU tensors."""
+    import torch
+    nbs, hkv, bs, d = src[0].shape
+    nbd = dst[0].shape[0]
+    _need(all(t.shape == src[0].shape for t in src[:2]) and all(t.shape == dst[0].shape for t in dst[:2]),
+          "shape mismatch")
+    _need(dst[0].shape[1:] == src[0].shape[1:], "pools must share Hkv, B, d")
+    _need(all(_cache_code(t) == PA_FP8_E4M3 for t in (src[0], src[1], dst[0], dst[1])) and
+          all(t.dtype == torch.float32 and t.shape == c.shape[:2]
+              for t, c in ((src[2], src[0]), (src[3], src[0]), (dst[2], dst[0]), (dst[3], dst[0]))),
+          "codes E4M3 [NB, Hkv, B, d], scales float32 [NB, Hkv]")
+    _need(block_mapping.dim() == 2 and block_mapping.shape[1] == 2, "block_mapping must be [n, 2]")
+    if device is None:
+        device = next((t.device for t in (src[0], dst[0]) if t.is_cuda), torch.device("cuda"))
+    names = ("k_cache", "v_cache", "k_scales", "v_scales")
+    st = lib().pa_swap_blocks_fp8_block(
+        *[_reachable(t, "src " + nm) for t, nm in zip(src, names)],
+        *[_reachable(t, "dst " + nm) for t, nm in zip(dst, names)],
+        _reachable(block_mapping, "block_mapping", torch.int32), block_mapping.shape[0], nbs, nbd,
+        hkv, d, bs, _stream_ptr(stream, device))
+    _check(st, "pa_swap_blocks_fp8_block")
 
 
 @_on_first

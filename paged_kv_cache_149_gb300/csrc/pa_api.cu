@@ -141,8 +141,9 @@ int decode_call(const void* q, const void* key_new, const void* value_new, const
                 int head_dim, int block_size, int num_blocks, float scale, void* out,
                 void* workspace, size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream,
                 bool kv_fp8 = false, float k_scale = 1.f, float v_scale = 1.f,
-                const float* k_scales = nullptr, const float* v_scales = nullptr) {
-  const bool kv_int4 = k_scales != nullptr || v_scales != nullptr;
+                const float* k_scales = nullptr, const float* v_scales = nullptr,
+                bool kv_fp8_block = false) {
+  const bool kv_int4 = !kv_fp8_block && (k_scales != nullptr || v_scales != nullptr);
   if (kv_int4 && (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)))
     return PA_ERR_ARG;
   if (kv_fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !(k_scale > 0.f) ||
@@ -189,6 +190,7 @@ int decode_call(const void* q, const void* key_new, const void* value_new, const
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.kv_int4 = kv_int4;
+  a.kv_fp8_block = kv_fp8_block;
   a.k_scales = k_scales;
   a.v_scales = v_scales;
   a.err = di.err;
@@ -355,6 +357,115 @@ int pa_swap_blocks_int4(const void* src_k, const void* src_v, const float* src_k
   st = pa::swap_blocks_launch(dev[2], dev[3], dev[6], dev[7], map, num_pairs, src_num_blocks,
                               dst_num_blocks, num_kv_heads, 4, block_size, di.err, stream);
   return st == 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- FP8 K/V blocks with block scales: codes [NB][Hkv][B][d] + float32 scales [NB][Hkv] ----
+
+namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool fp8_block_arrays_ok(const void* kc, const void* vc, const void* ks, const void* vs) {
+  return kc && vc && ks && vs && aligned16(kc) && aligned16(vc) && aligned4(ks) && aligned4(vs);
+}
+}  // namespace
+
+int pa_build_step(const int32_t* query_lens, const int32_t* context_lens, int num_seqs,
+                  const int32_t* free_blocks, int num_free, const int32_t* free_start,
+                  int32_t* block_tables, int max_blocks_per_seq, int block_size, int num_blocks,
+                  int64_t* slot_mapping, int num_slots, int32_t* query_start, int32_t* free_next,
+                  cudaStream_t stream) {
+  if (num_seqs < 0 || num_free < 0 || num_slots < 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      !shape_ok(1, 64, block_size) ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
+    return PA_ERR_ARG;
+  if (!free_start || !free_next || free_start == free_next || !query_start ||
+      (num_slots > 0 && !slot_mapping) || (num_free > 0 && !free_blocks) ||
+      (num_seqs > 0 && (!query_lens || !context_lens || !block_tables)))
+    return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  return pa::build_step_launch(query_lens, context_lens, num_seqs, free_blocks, num_free,
+                               free_start, block_tables, max_blocks_per_seq, block_size,
+                               num_blocks, slot_mapping, num_slots, query_start, free_next,
+                               di.sm_count, di.err, stream);
+}
+
+int pa_append_fp8_block(const void* key, const void* value, void* k_cache, void* v_cache,
+                        float* k_scales, float* v_scales, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* query_start, int num_seqs, int num_tokens, int num_blocks,
+                        int num_kv_heads, int head_dim, int block_size, pa_dtype dtype,
+                        cudaStream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      !shape_ok(num_kv_heads, head_dim, block_size) || (dtype != PA_FP16 && dtype != PA_BF16) ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL ||
+      static_cast<long long>(num_blocks) * num_kv_heads * block_size > 0x7fffffffLL)
+    return PA_ERR_ARG;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!key || !value || !block_tables || !context_lens || !query_start || !aligned16(key) ||
+      !aligned16(value) || !fp8_block_arrays_ok(k_cache, v_cache, k_scales, v_scales))
+    return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  return pa::append_fp8_block_launch(key, value, k_cache, v_cache, k_scales, v_scales,
+                                     block_tables, max_blocks_per_seq, context_lens, query_start,
+                                     num_seqs, num_tokens, num_blocks, num_kv_heads, head_dim,
+                                     block_size, dtype == PA_BF16, di.sm_count, di.err, stream);
+}
+
+int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                        int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                        int num_blocks, float scale, void* out, void* workspace,
+                        size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream) {
+  if (num_seqs > 0 && !fp8_block_arrays_ok(k_cache, v_cache, k_scales, v_scales))
+    return PA_ERR_ARG;
+  return decode_call(q, nullptr, nullptr, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                     context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                     num_blocks, scale, out, workspace, workspace_bytes, dtype, stream, false, 1.f,
+                     1.f, k_scales, v_scales, true);
+}
+
+int pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                             const int32_t* block_mapping, int num_pairs, int num_blocks,
+                             int num_kv_heads, int head_dim, int block_size,
+                             cudaStream_t stream) {
+  if (num_pairs < 0 || num_blocks < 1 || !shape_ok(num_kv_heads, head_dim, block_size))
+    return PA_ERR_ARG;
+  if (num_pairs == 0) return PA_OK;
+  if (!block_mapping || !fp8_block_arrays_ok(k_cache, v_cache, k_scales, v_scales))
+    return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  return pa::swap_blocks_scaled_launch(k_cache, v_cache, k_scales, v_scales, k_cache, v_cache,
+                                       k_scales, v_scales, block_mapping, num_pairs, num_blocks,
+                                       num_blocks, num_kv_heads, head_dim, block_size, di.err,
+                                       stream);
+}
+
+int pa_swap_blocks_fp8_block(const void* src_k, const void* src_v, const float* src_ks,
+                             const float* src_vs, void* dst_k, void* dst_v, float* dst_ks,
+                             float* dst_vs, const int32_t* block_mapping, int num_pairs,
+                             int src_num_blocks, int dst_num_blocks, int num_kv_heads,
+                             int head_dim, int block_size, cudaStream_t stream) {
+  if (num_pairs < 0 || src_num_blocks < 1 || dst_num_blocks < 1 ||
+      !shape_ok(num_kv_heads, head_dim, block_size))
+    return PA_ERR_ARG;
+  if (num_pairs == 0) return PA_OK;
+  const void* ptrs[9] = {src_k, src_v, dst_k, dst_v, src_ks, src_vs, dst_ks, dst_vs, block_mapping};
+  void* dev[9];
+  for (int i = 0; i < 9; ++i) {
+    dev[i] = device_view(ptrs[i]);
+    if (!dev[i] || (i < 4 ? !aligned16(dev[i]) : !aligned4(dev[i]))) return PA_ERR_ARG;
+  }
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  return pa::swap_blocks_scaled_launch(
+      dev[0], dev[1], static_cast<const float*>(dev[4]), static_cast<const float*>(dev[5]), dev[2],
+      dev[3], static_cast<float*>(dev[6]), static_cast<float*>(dev[7]),
+      static_cast<const int32_t*>(dev[8]), num_pairs, src_num_blocks, dst_num_blocks, num_kv_heads,
+      head_dim, block_size, di.err, stream);
 }
 
 int pa_prefill(const void* q, const void* k_cache, const void* v_cache,

@@ -172,10 +172,19 @@ constexpr int kCopyUnroll = 4;  // 16-byte loads in flight per thread before its
 // flight (host memory across the chip-to-chip link answers slower than HBM).  The source
 // and destination blocks of a pair never overlap (distinct pools, or, within one pool, a
 // checked pair list).  A pair with an id outside its pool is skipped and flagged.
+// SCALED: each block also has num_scales floats beside its codes (FP8 blocks with a scale per
+// kv head), copied by the first chunk's CTA.
+struct BlockScales {
+  const float *src_k, *src_v;
+  float *dst_k, *dst_v;
+  int num_scales;
+};
+
+template <bool SCALED>
 __global__ void __launch_bounds__(kCopyThreads) block_copy_kernel(
     const uint4* __restrict__ src_k, const uint4* __restrict__ src_v, uint4* __restrict__ dst_k,
     uint4* __restrict__ dst_v, const int32_t* __restrict__ mapping, int src_blocks,
-    int dst_blocks, size_t block_vecs, unsigned* err) {
+    int dst_blocks, size_t block_vecs, const BlockScales sc, unsigned* err) {
   const int pair = blockIdx.x;
   const int src = mapping[2 * pair];
   const int dst = mapping[2 * pair + 1];
@@ -185,6 +194,13 @@ __global__ void __launch_bounds__(kCopyThreads) block_copy_kernel(
   }
   const uint4* s = (blockIdx.z == 0 ? src_k : src_v) + static_cast<size_t>(src) * block_vecs;
   uint4* d = (blockIdx.z == 0 ? dst_k : dst_v) + static_cast<size_t>(dst) * block_vecs;
+  if constexpr (SCALED) {
+    if (blockIdx.y == 0) {
+      const float* ss = (blockIdx.z == 0 ? sc.src_k : sc.src_v) + static_cast<size_t>(src) * sc.num_scales;
+      float* ds = (blockIdx.z == 0 ? sc.dst_k : sc.dst_v) + static_cast<size_t>(dst) * sc.num_scales;
+      for (int h = threadIdx.x; h < sc.num_scales; h += kCopyThreads) ds[h] = ss[h];
+    }
+  }
   const size_t step = static_cast<size_t>(gridDim.y) * kCopyThreads;
   for (size_t j0 = static_cast<size_t>(blockIdx.y) * kCopyThreads + threadIdx.x; j0 < block_vecs;
        j0 += step * kCopyUnroll) {
@@ -201,15 +217,17 @@ __global__ void __launch_bounds__(kCopyThreads) block_copy_kernel(
 int block_copy_launch(const void* src_k, const void* src_v, void* dst_k, void* dst_v,
                       const int32_t* mapping, int num_pairs, int src_blocks, int dst_blocks,
                       int num_kv_heads, int row_bytes, int block_size, unsigned* err,
-                      cudaStream_t stream) {
+                      cudaStream_t stream, const BlockScales* scales = nullptr) {
   if (num_pairs == 0) return 0;
   const size_t block_vecs = static_cast<size_t>(num_kv_heads) * block_size * row_bytes / 16;
   const size_t per_cta = static_cast<size_t>(kCopyThreads) * kCopyUnroll;
   int chunks = static_cast<int>((block_vecs + per_cta - 1) / per_cta);
   if (chunks > 64) chunks = 64;
-  block_copy_kernel<<<dim3(num_pairs, chunks, 2), kCopyThreads, 0, stream>>>(
+  auto* kern = scales ? block_copy_kernel<true> : block_copy_kernel<false>;
+  kern<<<dim3(num_pairs, chunks, 2), kCopyThreads, 0, stream>>>(
       static_cast<const uint4*>(src_k), static_cast<const uint4*>(src_v), static_cast<uint4*>(dst_k),
-      static_cast<uint4*>(dst_v), mapping, src_blocks, dst_blocks, block_vecs, err);
+      static_cast<uint4*>(dst_v), mapping, src_blocks, dst_blocks, block_vecs,
+      scales ? *scales : BlockScales{}, err);
   return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
@@ -280,6 +298,16 @@ int swap_blocks_launch(const void* src_k, const void* src_v, void* dst_k, void* 
                        unsigned* err, cudaStream_t stream) {
   return block_copy_launch(src_k, src_v, dst_k, dst_v, block_mapping, num_pairs, src_num_blocks,
                            dst_num_blocks, num_kv_heads, row_bytes, block_size, err, stream);
+}
+
+int swap_blocks_scaled_launch(const void* src_k, const void* src_v, const float* src_ks,
+                              const float* src_vs, void* dst_k, void* dst_v, float* dst_ks,
+                              float* dst_vs, const int32_t* block_mapping, int num_pairs,
+                              int src_num_blocks, int dst_num_blocks, int num_kv_heads,
+                              int row_bytes, int block_size, unsigned* err, cudaStream_t stream) {
+  const BlockScales sc{src_ks, src_vs, dst_ks, dst_vs, num_kv_heads};
+  return block_copy_launch(src_k, src_v, dst_k, dst_v, block_mapping, num_pairs, src_num_blocks,
+                           dst_num_blocks, num_kv_heads, row_bytes, block_size, err, stream, &sc);
 }
 
 }  // namespace pa

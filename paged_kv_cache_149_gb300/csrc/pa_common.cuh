@@ -20,6 +20,7 @@ constexpr unsigned kErrBadContext = 0x2u;
 constexpr unsigned kErrBadSlot = 0x4u;
 constexpr unsigned kErrBadPair = 0x8u;
 constexpr unsigned kErrTimeout = 0x10u;
+constexpr unsigned kErrNoBlocks = 0x20u;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -106,6 +107,11 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// The same for the L2 line that holds one value.
+__device__ __forceinline__ void prefetch_l2_line(const void* src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -187,6 +193,13 @@ __device__ __forceinline__ uint16_t e4m3x2_of(float hi, float lo) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Two codes (the first in the lower byte) -> their values.
+__device__ __forceinline__ float2 e4m3x2_floats(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return unpack2<__half>(h);
 }
 
 // Sixteen 16-bit values (two 16-byte vectors, element 0 first) -> their 16 codes.

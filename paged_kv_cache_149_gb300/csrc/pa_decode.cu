@@ -56,7 +56,7 @@ int decode_launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   // a timeline buffer set: the stamped copy of the 16-bit kernel (pa_decode_timed.cu), for
   // head_dim 128 and up to 8 query heads a pair only
   if (t_timeline &&
-      (a.kv_fp8 || a.kv_int4 || a.head_dim != 128 ||
+      (a.kv_fp8 || a.kv_int4 || a.kv_fp8_block || a.head_dim != 128 ||
        decode_heads_per_pair(a.num_q_heads, a.num_kv_heads) > 8 ||
        t_timeline_bytes < static_cast<size_t>(grid) * decode::kWarps * 3 * sizeof(unsigned long long)))
     return -1;
@@ -84,7 +84,7 @@ int decode_launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   p.log2_block = a.block_size == 8 ? 3 : (a.block_size == 16 ? 4 : 5);
   p.num_blocks = a.num_blocks;
   p.max_ctx = a.max_blocks_per_seq * a.block_size;
-  const bool quantised = a.kv_fp8 || a.kv_int4;
+  const bool quantised = a.kv_fp8 || a.kv_int4 || a.kv_fp8_block;
   p.log2_stage = quantised ? 5 : 4;  // 32-token stages over quantised blocks, 16 over 16-bit ones
   // per-family charge (the same charge in tokens for 32-token stages)
   p.seg_cost = decode::seg_cost_for(static_cast<long long>(a.num_seqs) * p.ngroups, grid) >>
@@ -94,7 +94,7 @@ int decode_launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   p.out_scale = a.kv_fp8 ? a.v_scale : 1.f;
   p.k_quant = a.k_scale;
   p.v_quant = a.v_scale;
-  // INT4 blocks: a scale per row, applied in the kernel
+  // INT4 blocks: a scale per row, and FP8 blocks with block scales: applied in the kernel
   p.k_scales = static_cast<const float*>(a.k_scales);
   p.v_scales = static_cast<const float*>(a.v_scales);
   p.err = a.err;
@@ -119,6 +119,7 @@ int decode_launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   if (a.kv_int4)
     return fused ? decode::launch_format<decode::kKvInt4, true>(p, grid, a.head_dim, a.bf16, stream)
                  : decode::launch_format<decode::kKvInt4, false>(p, grid, a.head_dim, a.bf16, stream);
+  if (a.kv_fp8_block) return decode::launch_fp8_block(p, grid, a.head_dim, a.bf16, stream);
   if (t_timeline) return decode_launch_timed(p, grid, a.bf16, stream, t_timeline);
   return fused ? decode::launch_format<decode::kKv16, true>(p, grid, a.head_dim, a.bf16, stream)
                : decode::launch_format<decode::kKv16, false>(p, grid, a.head_dim, a.bf16, stream);

@@ -115,10 +115,14 @@ inline int seg_cost_for(long long families, int shares) {
 }
 
 // Cached K/V formats: 16-bit values, FP8 (E4M3) codes with one scale per cache, INT4
-// codes (two per byte) with one float32 scale per row.
+// codes (two per byte) with one float32 scale per row, FP8 codes with one float32 scale per
+// (block, kv head).
 constexpr int kKv16 = 0;
 constexpr int kKvFp8 = 1;
 constexpr int kKvInt4 = 2;
+constexpr int kKvFp8Block = 3;
+template <int KV>
+constexpr bool kFp8Codes = KV == kKvFp8 || KV == kKvFp8Block;
 
 // A stage of quantised blocks holds 32 tokens, so the per-stage work that does not scale
 // with bytes (softmax reductions, bookkeeping) is paid once per 32 tokens.  INT4 stages
@@ -126,7 +130,7 @@ constexpr int kKvInt4 = 2;
 template <int D, int KV = kKv16>
 struct Geo {
   static constexpr int kTok = KV == kKv16 ? kStageTok : 2 * kStageTok;  // tokens per stage
-  static constexpr int kRowBytes = KV == kKv16 ? 2 * D : (KV == kKvFp8 ? D : D / 2);
+  static constexpr int kRowBytes = KV == kKv16 ? 2 * D : (kFp8Codes<KV> ? D : D / 2);
   static constexpr int kRowChunks = kRowBytes / 16;         // 16-byte chunks per row
   static constexpr int kKBytes = kTok * kRowBytes;          // K rows of a stage
   static constexpr int kScaleBytes = KV == kKvInt4 ? 4 * kTok : 0;  // K (or V) row scales
@@ -161,7 +165,8 @@ struct Params {
   float scale_log2;
   float out_scale;  // FP8 blocks: v_scale, applied to every output row (else 1)
   float k_quant, v_quant;  // FP8 blocks: k_scale, v_scale for the fused step's newest rows
-  // INT4 blocks: float32 scale of each cached row, [num_blocks][Hkv][B] (else null)
+  // INT4 blocks: float32 scale of each cached row, [num_blocks][Hkv][B]; FP8 blocks with
+  // block scales: of each block and kv head, [num_blocks][Hkv] (else null)
   const float* k_scales;
   const float* v_scales;
   // [grid][gs]: arrivals at cut pair (first CTA, pi): epoch tag << 24 | pieces counted in
@@ -309,6 +314,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(src_bytes)
                : "memory");
+}
+// The same for one float (4-byte aligned; this size goes through L1).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -856,7 +865,10 @@ template <int D, int KV>
 struct Smem {
   uint8_t ring[kWarps][Geo<D, KV>::kSlots][Geo<D, KV>::kStageBytes];  // 1024-byte aligned
   // quantised blocks, fused step: the newest token's 16-bit K and V rows, per ring slot
-  uint8_t newrow[kWarps][Geo<D, KV>::kSlots][KV == kKv16 ? 16 : 4 * D];
+  uint8_t newrow[kWarps][Geo<D, KV>::kSlots][KV == kKv16 || KV == kKvFp8Block ? 16 : 4 * D];
+  // FP8 blocks with block scales, per ring slot: the K scales of the stage's four groups of
+  // eight tokens, then their V scales
+  float bscale[KV == kKvFp8Block ? kWarps : 1][Geo<D, KV>::kSlots][KV == kKvFp8Block ? 8 : 1];
   float xo[kWarps][4][D];  // per-warp O rows, 4 heads per exchange round
   float xm[kWarps][kMaxHeads], xl[kWarps][kMaxHeads];
   long long scan[kWarps];
@@ -958,6 +970,13 @@ __device__ __forceinline__ bool next_busy_fam(Fam f, int pi, long long w0, long 
 }
 
 // KV = kKvFp8: K/V blocks hold E4M3 codes (scales folded into scale_log2 and out_scale).
+// KV = kKvFp8Block: E4M3 codes with a float32 scale per (block, kv head).  Eight tokens never
+// straddle a block, so a stage has four groups of tokens with one K and one V scale each,
+// and a lane's scores of one (m-tile, half) lie in one group: the K scale is one factor of
+// each score.  The V scale vs multiplies the weights before they are rounded to f16 for P V,
+// relative to the largest scale V_ref that the warp has met (2^-k <= 1, exact for the powers
+// of two that the cache write stores), so that no scale over- or underflows f16; O holds
+// sums over V_ref, rescaled with the running maximum when V_ref grows.
 // KV = kKvInt4: K/V blocks hold INT4 codes with a float32 scale per row: a token's K scale
 // multiplies its scores, its V scale its weights in P V.  Both quantised formats run the
 // MMAs in f16 on values widened exactly, with 32-token stages and the permuted d order of
@@ -967,7 +986,8 @@ __device__ __forceinline__ bool next_busy_fam(Fam f, int pi, long long w0, long 
 template <int D, int NTH, typename T, int KV, bool NEW>
 __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_constant__ Params p
                                                                   PA_DECODE_TIMELINE_ARG) {
-  constexpr bool F8 = KV == kKvFp8;
+  constexpr bool F8 = kFp8Codes<KV>;
+  constexpr bool FB = KV == kKvFp8Block;
   constexpr bool I4 = KV == kKvInt4;
   constexpr bool QK = KV != kKv16;  // quantised blocks
   using G_ = Geo<D, KV>;
@@ -1160,6 +1180,19 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
                        (isv ? p.value_new : p.key_new) + nsrc, 16u);
           }
         }
+        if constexpr (FB) {
+          // lane g < 4: the K scale of token group g's block, lane 4 + g: its V scale (a
+          // group past the context repeats the first block's)
+          if (lane < 8) {
+            const int kk = (8 * (lane & 3)) >> p.log2_block;
+            int e = nxt_e[0];
+#pragma unroll
+            for (int k = 1; k < NE; ++k) e = kk == k ? nxt_e[k] : e;
+            cp_async4(smem_addr(&sm.bscale[warp][slot][lane]),
+                      (lane < 4 ? p.k_scales : p.v_scales) +
+                          static_cast<size_t>(e) * p.num_kv_heads + nxt.kvh);
+          }
+        }
         if constexpr (I4) {
           // the rows' scales: lanes 0-7 copy K's, 8-15 V's, four tokens (16 bytes) each; a
           // token past the context gets scale 0 (its codes are zero-filled too)
@@ -1207,6 +1240,11 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
         if constexpr (I4) {
           prefetch_l2(p.k_scales + row, 4u * p.block_size);
           prefetch_l2(p.v_scales + row, 4u * p.block_size);
+        }
+        if constexpr (FB) {
+          const size_t group = static_cast<size_t>(e) * p.num_kv_heads + nxt.kvh;
+          prefetch_l2_line(p.k_scales + group);
+          prefetch_l2_line(p.v_scales + group);
         }
       }
     }
@@ -1316,6 +1354,8 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
     bool seg_bad = false;
+    // FB: the largest V scale met so far (O holds sums over it), and its reciprocal
+    float v_ref = 0.f, v_inv = 0.f;
 
     const int j_first = r.x + (phase - r.x % P + P) % P;
     for (int j = j_first; j < r.y; j += P) {
@@ -1399,6 +1439,27 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
               ksc[u][hr] = lds_f32(sa);
               vsc[u][hr] = lds_f32(sa + G_::kScaleBytes);
             }
+        }
+        // FB: the K scale (with the softmax scale) and the relative V scale of the tokens
+        // 16u + 8 hr .. + 7, and the factor that brings O to a grown V_ref
+        float bks[U][2], bvs[U][2], v_fac = 1.f;
+        if constexpr (FB) {
+          const float4 sk = *reinterpret_cast<const float4*>(&sm.bscale[warp][slot][0]);
+          const float4 sv = *reinterpret_cast<const float4*>(&sm.bscale[warp][slot][4]);
+          const float top = fmaxf(v_ref, fmaxf(fmaxf(sv.x, sv.y), fmaxf(sv.z, sv.w)));
+          if (top > v_ref) {  // (uniform over the warp)
+            v_inv = __frcp_rn(top);
+            v_fac = v_ref * v_inv;
+            v_ref = top;
+          }
+          bks[0][0] = sk.x * p.scale_log2;
+          bks[0][1] = sk.y * p.scale_log2;
+          bks[U - 1][0] = sk.z * p.scale_log2;
+          bks[U - 1][1] = sk.w * p.scale_log2;
+          bvs[0][0] = sv.x * v_inv;
+          bvs[0][1] = sv.y * v_inv;
+          bvs[U - 1][0] = sv.z * v_inv;
+          bvs[U - 1][1] = sv.w * v_inv;
         }
         if constexpr (I4) {
           // K rows 16u + r0 and + 8, bytes [(D/8) t, (D/8)(t+1)): word j holds the eight d
@@ -1501,7 +1562,9 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float v = (sacc[u][nt][e] + sodd[u][nt][e]) *
-                              (I4 ? ksc[u][e >> 1] * p.scale_log2 : p.scale_log2);
+                              (I4   ? ksc[u][e >> 1] * p.scale_log2
+                               : FB ? bks[u][e >> 1]
+                                    : p.scale_log2);
               x[u][e] = 16 * u + r0 + (e < 2 ? 0 : 8) < nt_tok ? v : -INFINITY;
             }
           float pr[U][4];
@@ -1534,7 +1597,8 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           for (int u = 0; u < U; ++u) {
             // (INT4: each token's weight times its V scale; the sums l keep the weights,
             // W the rounded products that enter P V)
-            const float v0 = I4 ? vsc[u][0] : 1.f, v1 = I4 ? vsc[u][1] : 1.f;
+            const float v0 = I4 ? vsc[u][0] : (FB ? bvs[u][0] : 1.f);
+            const float v1 = I4 ? vsc[u][1] : (FB ? bvs[u][1] : 1.f);
             const uint32_t w01 = pack2<TM>(pr[u][0] * v0, pr[u][1] * v0);  // tokens 16u + 0-7
             const uint32_t w23 = pack2<TM>(pr[u][2] * v1, pr[u][3] * v1);  // tokens 16u + 8-15
             if constexpr (I4) {
@@ -1548,6 +1612,13 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           if constexpr (I4) {
             wsum[nt][0] = fmaf(wsum[nt][0], alpha[nt][0], wst0);
             wsum[nt][1] = fmaf(wsum[nt][1], alpha[nt][1], wst1);
+          }
+        }
+        if constexpr (FB) {
+#pragma unroll
+          for (int nt = 0; nt < NTH; ++nt) {
+            alpha[nt][0] *= v_fac;
+            alpha[nt][1] *= v_fac;
           }
         }
         bool all_one = true;
@@ -1699,6 +1770,15 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
         }
     }
     const bool whole = r.x == 0 && r.y == f.ns;
+    if constexpr (FB) {
+      // O in the values' own units (pieces and the warps of a pair have V_refs of their own)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= v_ref;
+    }
     const int slot_out = cta_first ? 0 : 1;
     const size_t piece = (static_cast<size_t>(c) * 2 + slot_out) * p.gs + pi;
     float* pacc = p.part_acc + piece * p.heads_per_pair * D;
@@ -1949,6 +2029,9 @@ int PA_DECODE_LAUNCH(const Params& prm, int grid, cudaStream_t stream PA_DECODE_
 }
 
 #ifndef PA_DECODE_TIMELINE
+// FP8 blocks with block scales, plain decode (pa_decode_fp8_block.cu).
+int launch_fp8_block(const Params& p, int grid, int head_dim, bool bf16, cudaStream_t stream);
+
 // Every kernel of one K/V format, for the plain decode (NEW false) or the fused step (NEW
 // true): head_dim 128 or 64, one n-tile of heads or two, bf16 or fp16.  Each (format, NEW)
 // is instantiated in a translation unit of its own, so that the six compile in parallel:

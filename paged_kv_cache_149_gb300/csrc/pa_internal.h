@@ -25,7 +25,8 @@ struct DecodeArgs {
   bool kv_fp8;     // caches hold FP8 E4M3 codes with scales k_scale, v_scale
   float k_scale = 1.f, v_scale = 1.f;
   bool kv_int4 = false;  // caches hold INT4 codes [NB][Hkv][B][d/2] with a scale per row
-  const void* k_scales = nullptr;  // INT4: float32 [NB][Hkv][B]
+  bool kv_fp8_block = false;  // caches hold FP8 codes with a scale per (block, kv head)
+  const void* k_scales = nullptr;  // INT4: float32 [NB][Hkv][B]; kv_fp8_block: [NB][Hkv]
   const void* v_scales = nullptr;
   unsigned* err;  // device address of the per-device error word
 };
@@ -77,6 +78,25 @@ int cache_int4_launch(const void* key, const void* value, void* k_codes, void* v
                       float* k_scales, float* v_scales, const int64_t* slot_mapping,
                       int num_tokens, int num_blocks, int num_kv_heads, int head_dim,
                       int block_size, bool bf16, unsigned* err, cudaStream_t stream);
+// The step's block tables and slots from request lengths (pa_build_step).
+int build_step_launch(const int32_t* query_lens, const int32_t* context_lens, int num_seqs,
+                      const int32_t* free_blocks, int num_free, const int32_t* free_start,
+                      int32_t* block_tables, int max_blocks_per_seq, int block_size,
+                      int num_blocks, int64_t* slot_mapping, int num_slots, int32_t* query_start,
+                      int32_t* free_next, int sm_count, unsigned* err, cudaStream_t stream);
+// FP8 cache write with a scale per (block, kv head), through the block tables.
+int append_fp8_block_launch(const void* key, const void* value, void* k_cache, void* v_cache,
+                            float* k_scales, float* v_scales, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* context_lens,
+                            const int32_t* query_start, int num_seqs, int num_tokens,
+                            int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                            bool bf16, int sm_count, unsigned* err, cudaStream_t stream);
+// swap_blocks_launch for FP8 blocks with block scales: codes and scales in one launch.
+int swap_blocks_scaled_launch(const void* src_k, const void* src_v, const float* src_ks,
+                              const float* src_vs, void* dst_k, void* dst_v, float* dst_ks,
+                              float* dst_vs, const int32_t* block_mapping, int num_pairs,
+                              int src_num_blocks, int dst_num_blocks, int num_kv_heads,
+                              int row_bytes, int block_size, unsigned* err, cudaStream_t stream);
 int swap_blocks_launch(const void* src_k, const void* src_v, void* dst_k, void* dst_v,
                        const int32_t* block_mapping, int num_pairs, int src_num_blocks,
                        int dst_num_blocks, int num_kv_heads, int row_bytes, int block_size,
