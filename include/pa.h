@@ -320,6 +320,18 @@ int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                         int num_blocks, float scale, void* out, void* workspace,
                         size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream);
+/* pa_prefill over those blocks: the arguments and rules of pa_prefill, K and V the values
+ * decode(code) * scale of each token's block.  The kernel widens them to `dtype`: exactly
+ * where the scale is a power of two and the value lies in the type's range, else rounded to
+ * nearest-even, magnitudes above its largest value clamped to it.  Write the sequences'
+ * new tokens first (pa_append_fp8_block). */
+int pa_prefill_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                         const float* k_scales, const float* v_scales,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* query_start, int num_seqs,
+                         int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, float scale, void* out, pa_dtype dtype,
+                         cudaStream_t stream);
 /* pa_copy_blocks for those blocks: codes and scales of each pair, in one launch. */
 int pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
                              const int32_t* block_mapping, int num_pairs, int num_blocks,

@@ -76,6 +76,8 @@ SIGNATURES = {
                                    _i32, _i32, _i32, _i32, _i32, _vp]),
     "pa_decode_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _vp, _vp, _sz, _i32, _vp]),
+    "pa_prefill_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
+                                    _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp]),
     "pa_copy_blocks_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                         _vp]),
     "pa_swap_blocks_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
@@ -802,6 +804,36 @@ def decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, cont
                       keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                             workspace))
     _check(lib().pa_decode_fp8_block(*args, _stream_ptr(stream, q.device)), "pa_decode_fp8_block")
+    return out
+
+
+@_on_first
+def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                      query_start, scale, max_query_len, out=None, stream=None, plan=False):
+    """prefill over FP8 blocks with a scale per (block, kv head): causal attention of each
+    sequence's newest tokens over its paged context; the tokens' own rows must already be in
+    the cache (append_fp8_block).  plan=True returns a Launch instead of launching."""
+    import torch
+    ntok, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    n = context_lens.shape[0]
+    _need(v_cache.shape == k_cache.shape and d == d2, "shape mismatch")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
+    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    args = (_dev(q, "q"), kc, vc, ks, vs, _dev(block_tables, "block_tables", torch.int32),
+            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32),
+            _dev(query_start, "query_start", torch.int32), n, int(max_query_len), hq, hkv, d, bs,
+            nb, float(scale), _dev(out, "out"), _dtype_code(q))
+    if plan:
+        return Launch("pa_prefill_fp8_block", args, out,
+                      keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                            query_start))
+    _check(lib().pa_prefill_fp8_block(*args, _stream_ptr(stream, q.device)), "pa_prefill_fp8_block")
     return out
 
 

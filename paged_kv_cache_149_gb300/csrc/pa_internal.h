@@ -54,6 +54,8 @@ struct PrefillArgs {
   float scale;
   bool bf16;
   unsigned* err;
+  const float* k_scales = nullptr;  // FP8 blocks with block scales: [NB][Hkv]
+  const float* v_scales = nullptr;
 };
 
 // Launch the paged prefill kernel; 0 or a negative PA_ERR_* code.

@@ -68,7 +68,17 @@ constexpr int kTableAhead = 4;  // tiles the loader looks block-table entries up
 constexpr int kLoadWarp = 8;    // loads Q and the K tiles
 constexpr int kLoadWarpV = 11;  // loads the V tiles
 constexpr int kMmaWarp = 9;     // MMA issue for tile 0; tile 1 has the next warp
-constexpr int kThreads = 384;   // 2 x 128 softmax threads, two loader warps, two MMA warps
+// 2 x 128 softmax threads, two loader warps, two MMA warps; over FP8 blocks a fourth
+// warpgroup that widens codes (then the loader warps load Q alone)
+template <bool KV8>
+constexpr int kThreadsOf = KV8 ? 512 : 384;
+constexpr int kWidenWarp = 12;  // the first of kWidenWarps
+constexpr int kWidenWarps = 4;
+// Registers over FP8 blocks: 512 threads launch with 128 each; the softmax warpgroups, which
+// hold a row of scores, take 160 and the other two keep 96 (2 x 160 + 2 x 96 = 4 x 128;
+// 168 + 88 and 152 + 104 make one side spill).
+constexpr int kSoftmaxRegs = 160;
+constexpr int kOtherRegs = 96;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that forces a rescale of O
 
@@ -89,6 +99,8 @@ struct Params {
   int ncb;  // query blocks (of kTiles x tpt tokens) of the longest sequence
   float scale_log2;
   unsigned* err;
+  const float* k_scales;  // FP8 blocks: [num_blocks][Hkv], else null
+  const float* v_scales;
 };
 
 template <int D>
@@ -251,8 +263,40 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       : "memory");
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p) {
+// Two values of a type in one word, magnitudes above its largest clamped to it.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_sat(float2 v) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  else
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+
+// Eight codes (two words) times a scale -> eight 16-bit values.
+template <typename T>
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, float scale) {
+  const float2 s2 = make_float2(scale, scale);
+  uint4 w;
+  w.x = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(lo)), s2));
+  w.y = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(lo >> 16)), s2));
+  w.z = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(hi)), s2));
+  w.w = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(hi >> 16)), s2));
+  return w;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// KV8: the caches hold FP8 (E4M3) codes with a scale per (block, kv head).  Four warps widen
+// them to 16-bit tiles in shared memory; the rest of the kernel is the same.
+template <int D, typename T, bool KV8>
+__global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __grid_constant__ Params p) {
+  constexpr int kThreads = kThreadsOf<KV8>;
   constexpr int CH = D / 8;                  // 16-byte chunks of a 16-bit row
   constexpr int KS1 = D / 16;                // MMA k-steps of S = Q K^T
   constexpr int KS2 = kKeys / 16;            // MMA k-steps of P V
@@ -307,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (tid == 0) {
     mbar_init(smem_addr(&sm.q_full), 33);  // TMA expect-tx + 32 copy lanes
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&sm.kv_full[i]), 66);  // per loader: TMA expect-tx + 32 copy lanes
+      // per loader: TMA expect-tx + 32 copy lanes; KV8: every lane that widens
+      mbar_init(smem_addr(&sm.kv_full[i]), KV8 ? 32 * kWidenWarps : 66);
     }
     for (int t = 0; t < kTiles; ++t)
       for (int b = 0; b < 2; ++b) {
@@ -338,13 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     return false;
   };
 
-  if (warp == kLoadWarp || warp == kLoadWarpV) {
+  if (warp >= kLoadWarp) {
+  if constexpr (KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kLoadWarp || warp >= kLoadWarpV) {
     // ===== loaders: Q once (the K loader), then the K (or V) tiles of the ring =====
     // Two warps, because one thread issuing TMA copies moves only about 26 GB/s per SM:
     // with one loader a 64-key step of both query tiles (32 KB of K and V) took about 2200
     // cycles to issue, against about 1300 cycles of tensor work.
     const bool is_v = warp == kLoadWarpV;
-    if (!is_v) {
+    if (warp == kLoadWarp) {
       // Q of both tiles: a whole tile (tpt tokens x G heads = 128 rows, each token's G rows
       // contiguous in q) by TMA, one copy per 64-column half; a tile that runs past the
       // sequence by 16-byte copies, zero-filled past its last token (token-major, no
@@ -383,6 +430,79 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       cp_async_arrive(smem_addr(&sm.q_full));
     }
+    if constexpr (KV8) {
+      if (warp >= kWidenWarp) {
+      // FP8 blocks: widening warp cw takes rows 16 cw .. 16 cw + 15 of every K and V tile
+      // (two groups of eight rows; eight rows never straddle a block).  A lane holds 16 codes
+      // of a row per load; the codes and scales of the next tile are fetched into the same
+      // registers as soon as this tile's are widened, its table entries a tile earlier.  Each code becomes
+      // the 16-bit value code * scale (exact for a power of two inside the type's range,
+      // otherwise rounded, and clamped to the type's largest), so the tiles, the MMAs and the
+      // softmax are those of 16-bit blocks.
+      constexpr int CPR = D / 16;    // 16-code chunks of a row
+      constexpr int RPI = 32 / CPR;  // rows a warp fetches at once
+      constexpr int NI = 16 / RPI;
+      const int cw = warp - kWidenWarp;
+      const int col = lane % CPR, rsub = lane / CPR;
+      const int log2b = 31 - __clz(p.block_size);
+      const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+      auto entry = [&](int kt, int grp) -> int {  // -1 past the keys or the context
+        const int pos = kt * kKeys + 16 * cw + 8 * grp;
+        return kt < n && pos < ctx ? __ldg(trow + (pos >> log2b)) : -1;
+      };
+      // this warp's codes of a tile of one cache, and its two groups' scales
+      auto fetch = [&](const uint8_t* cache, const float* scales, int kt, const int (&e)[2],
+                       uint4 (&c)[NI], float (&sc)[2]) {
+        const int pos0 = kt * kKeys + 16 * cw;
+#pragma unroll
+        for (int grp = 0; grp < 2; ++grp) {
+          const bool used = kt < n && pos0 + 8 * grp < ctx;
+          const bool ok = used && e[grp] >= 0 && e[grp] < p.num_blocks;
+          if (used && !ok && lane == 0) sm.bad = 1;
+          const size_t group = static_cast<size_t>(ok ? e[grp] : 0) * p.num_kv_heads + g;
+          sc[grp] = ok ? __ldg(scales + group) : 0.f;
+#pragma unroll
+          for (int i = grp * NI / 2; i < (grp + 1) * NI / 2; ++i) {
+            const int pos = pos0 + i * RPI + rsub;
+            const size_t at = ((group << log2b) + (pos & (p.block_size - 1))) * D + col * 16;
+            c[i] = ok && pos < ctx ? __ldg(reinterpret_cast<const uint4*>(cache + at)) : make_uint4(0, 0, 0, 0);
+          }
+        }
+      };
+      // 16 values as two 16-byte chunks of the tile's row; lanes of the right 64-column half
+      // store the odd chunk first, so the eight lanes of a row meet eight bank groups
+      auto put = [&](uint32_t tile, int row, const uint4& c, float scale) {
+        const uint4 a = widen8<T>(c.x, c.y, scale), b = widen8<T>(c.z, c.w, scale);
+        const bool odd = 2 * col >= 8;
+        st_shared16(tile + swz(kKeys, row, 2 * col + (odd ? 1 : 0)), odd ? b : a);
+        st_shared16(tile + swz(kKeys, row, 2 * col + (odd ? 0 : 1)), odd ? a : b);
+      };
+      uint4 ck[NI], cv[NI];
+      float sk[2], sv[2];
+      int e[2] = {entry(0, 0), entry(0, 1)};
+      fetch(p.k_cache, p.k_scales, 0, e, ck, sk);
+      fetch(p.v_cache, p.v_scales, 0, e, cv, sv);
+      e[0] = entry(1, 0);
+      e[1] = entry(1, 1);
+      for (int kt = 0; kt < n; ++kt) {
+        const int st = kt % kStages;
+        if (kt >= kStages && !(wait(sm.o_done[0][st], ((kt - kStages) / kStages) & 1) &&
+                               wait(sm.o_done[1][st], ((kt - kStages) / kStages) & 1)))
+          break;
+        const uint32_t kb = smem_addr(sm.k[st]), vb = smem_addr(sm.v[st]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) put(kb, 16 * cw + i * RPI + rsub, ck[i], sk[i * RPI / 8]);
+        fetch(p.k_cache, p.k_scales, kt + 1, e, ck, sk);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) put(vb, 16 * cw + i * RPI + rsub, cv[i], sv[i * RPI / 8]);
+        fetch(p.v_cache, p.v_scales, kt + 1, e, cv, sv);
+        e[0] = entry(kt + 2, 0);
+        e[1] = entry(kt + 2, 1);
+        fence_async_smem();  // these stores before the tensor cores' reads
+        mbar_arrive(smem_addr(&sm.kv_full[st]));
+      }
+      }
+    } else {
     const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
     const CUtensorMap* tmap = is_v ? &p.vmap : &p.kmap;
     const int B = p.block_size, nbk = kKeys / B;
@@ -445,8 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       cp_async_arrive(smem_addr(&sm.kv_full[st]));
     }
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+  } else {
     // ============ MMA issue: one thread per query tile (issue cost is per thread) ============
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16<T>(kRows, kKeys, false);
@@ -514,7 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       wait(sm.fin, 0);
     }
     __syncwarp();
+  }
   } else {
+    if constexpr (KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ================= softmax: warpgroup t, one thread per row =================
     const int t = warp >> 2, r = tid & (kRows - 1);
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + t * kTileCols;
@@ -679,10 +802,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
 }
 
-template <int D, typename T>
+template <int D, typename T, bool KV8>
 int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<D>) + 1024;
-  auto* kern = prefill_kernel<D, T>;
+  auto* kern = prefill_kernel<D, T, KV8>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return -3;
   cudaLaunchConfig_t cfg = {};
   const int per_cta = kTiles * prm.tpt;
@@ -692,7 +815,7 @@ int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
   // x: a block within its half (the later half has ceil(ncb / 2)), y: sequence,
   // z: half x kv head
   cfg.gridDim = dim3((ncb + 1) / 2, prm.num_seqs, 2 * prm.num_kv_heads);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreadsOf<KV8>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -764,11 +887,14 @@ static bool q_map(CUtensorMap* map, const void* q, int hq, int d, int g, long lo
 
 int prefill_launch(const PrefillArgs& a, cudaStream_t stream) {
   prefill::Params p;
-  if (!kv_cache_map(&p.kmap, a.k_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
-                    a.head_dim) ||
-      !kv_cache_map(&p.vmap, a.v_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
-                    a.head_dim))
+  const bool kv8 = a.k_scales != nullptr;
+  if (!kv8 && (!kv_cache_map(&p.kmap, a.k_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
+                             a.head_dim) ||
+               !kv_cache_map(&p.vmap, a.v_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
+                             a.head_dim)))
     return -3;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
   p.q = static_cast<const uint8_t*>(a.q);
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);
   p.v_cache = static_cast<const uint8_t*>(a.v_cache);
@@ -789,12 +915,15 @@ int prefill_launch(const PrefillArgs& a, cudaStream_t stream) {
                   static_cast<long long>(a.num_seqs) * a.max_query_len)
                 ? 1 : 0;
   p.err = a.err;
-  if (a.head_dim == 128)
-    return a.bf16 ? prefill::launch<128, __nv_bfloat16>(p, a.max_query_len, stream)
-                  : prefill::launch<128, __half>(p, a.max_query_len, stream);
-  if (a.head_dim == 64)
-    return a.bf16 ? prefill::launch<64, __nv_bfloat16>(p, a.max_query_len, stream)
-                  : prefill::launch<64, __half>(p, a.max_query_len, stream);
+#define PA_PREFILL_CASE(DD, K8)                                                         \
+  if (a.head_dim == DD && kv8 == K8)                                                    \
+    return a.bf16 ? prefill::launch<DD, __nv_bfloat16, K8>(p, a.max_query_len, stream)  \
+                  : prefill::launch<DD, __half, K8>(p, a.max_query_len, stream);
+  PA_PREFILL_CASE(128, false)
+  PA_PREFILL_CASE(64, false)
+  PA_PREFILL_CASE(128, true)
+  PA_PREFILL_CASE(64, true)
+#undef PA_PREFILL_CASE
   return -1;
 }
 

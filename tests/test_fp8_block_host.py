@@ -64,6 +64,14 @@ def test_decode_refusals(libpa, bad):
     assert libpa.lib().pa_decode_fp8_block(*decode_args(**bad)) == libpa.PA_ERR_ARG
 
 
+@pytest.mark.parametrize("bad", BAD_ATTENTION + [dict(most=-1), dict(qs=None), dict(hq=130)])
+def test_prefill_refusals(libpa, bad):
+    a = dict(q=P, kc=P, vc=P, ks=P, vs=P, tables=P, T=T, c=P, qs=P, n=N, most=9, hq=HQ, hkv=HKV, d=D,
+             B=B, nb=NB, scale=0.1, out=P, dtype=1)
+    a.update(bad)
+    assert libpa.lib().pa_prefill_fp8_block(*a.values(), None) == libpa.PA_ERR_ARG
+
+
 def test_copy_and_swap_refusals(libpa):
     lib = libpa.lib()
     for bad in (dict(d=96), dict(B=9), dict(n=-1), dict(nb=0), dict(kc=None), dict(ks=None),
@@ -99,6 +107,7 @@ def test_planned_launches_hold_their_tensors(cpu_marshal):
     q = torch.zeros(N, HQ, D, dtype=torch.bfloat16)
     made = [pa.append_fp8_block(rows, rows.clone(), *cache(), tables, lens, qs, plan=True),
             pa.decode_fp8_block(q, *cache(), tables, lens, 0.1, plan=True),
+            pa.prefill_fp8_block(q, *cache(), tables, lens, qs, 0.1, 1, plan=True),
             pa.build_step(lens, lens.clone(), torch.zeros(NB, **i32), torch.zeros(1, **i32), tables, B,
                           NB, torch.zeros(9, dtype=torch.int64), qs, torch.zeros(1, **i32), plan=True)]
     for launch in made:
@@ -131,6 +140,7 @@ def test_shape_and_type_checks_name_the_argument(cpu_marshal):
 
 
 def test_calls_make_their_tensors_device_current(libpa):
-    for name in ("build_step", "append_fp8_block", "decode_fp8_block", "copy_blocks_fp8_block",
+    for name in ("build_step", "append_fp8_block", "decode_fp8_block", "prefill_fp8_block",
+                 "copy_blocks_fp8_block",
                  "swap_blocks_fp8_block"):
         assert hasattr(getattr(libpa, name), "__wrapped__"), name

@@ -1,6 +1,6 @@
 """FP8 blocks with a scale per (block, kv head) on the GPU: the cache write is bit-exact against
 the oracle in every form a batch takes; decode is within the bound of its arithmetic of the
-float64 oracle over the same codes; block moves are exact; and the calls run together as a
+float64 oracle over the same codes, and so is prefill; block moves are exact; and the calls run together as a
 serving loop makes them."""
 import numpy as np
 import pytest
@@ -239,6 +239,82 @@ def test_decode_graph_stream_and_workspace():
     assert device_error() == 0
 
 
+# ------------------------------------------------------------------------------ prefill
+
+def check_prefill(b, new, caches, most=None, scale=None, pad=0):
+    """The newest new[s] tokens of every sequence as queries, with `pad` rows behind them."""
+    scale = 1.0 / np.sqrt(b.d) if scale is None else scale
+    qs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q_bits = rows16(b.rng, (int(qs[-1]) + pad, b.hq, b.d), b.dtype)
+    out = torch.full((len(q_bits), b.hq, b.d), 7.0, dtype=DTYPE[b.dtype], device="cuda")
+    pa.prefill_fp8_block(dev16(q_bits, b.dtype), *upload(caches), dev(b.tables), dev(b.ctx), dev(qs),
+                         scale, int(max(new)) if most is None else most, out=out)
+    assert device_error() == 0
+    got, q = values(out, b.dtype), decode_bits(q_bits, b.dtype)
+    assert (got[int(qs[-1]):] == 7).all()  # rows behind the last sequence stay
+    want = fb.paged_prefill(q, *caches, b.tables, b.ctx, qs, scale)
+    step = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[b.dtype]  # the weights' own rounding before P V
+    for s, c in enumerate(b.ctx):
+        k = fb.logical_rows(caches[0], caches[2], b.tables[s], c)
+        v = fb.logical_rows(caches[1], caches[3], b.tables[s], c)
+        for i in sorted({0, 1, new[s] // 2, new[s] - 2, new[s] - 1} & set(range(new[s]))):
+            n = c - (new[s] - 1 - i)
+            row = qs[s] + i
+            off = np.abs(got[row] - want[row])
+            most_off = bound(q[row], k[:n], v[:n], scale, want[row], b.dtype, step)
+            assert (off <= most_off).all(), (s, c, i, float((off / most_off).max()))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("B", [8, 16, 32])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 128), (8, 2, 64), (7, 1, 128), (12, 4, 128), (16, 1, 64)])
+def test_prefill_shapes(dtype, B, hq, hkv, d):
+    """Prompts from scratch and chunks, lengths around the tiles and blocks."""
+    ctx = [1, B, 63, 64, 65, 129, 200, 333]
+    new = [1, B, 5, 64, 65, 129, 77, 1]
+    b = Batch(ctx, hq, hkv, d, B, dtype, seed=hq * B, spread=2)
+    check_prefill(b, new, b.written(), pad=3)
+
+
+def test_prefill_long_context_short_query():
+    b = Batch([2500, 1030], 8, 2, 128, 16, "bf16", seed=3)
+    check_prefill(b, [3, 200], b.written())
+
+
+def test_prefill_with_empty_and_invalid_sequences():
+    b = Batch([40, 70, 90, 30], 4, 2, 64, 16, "fp16", seed=5, T=6)
+    caches = b.written()
+    new = [0, 70, 20, 30]
+    qs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    ctx, tables = b.ctx.copy(), b.tables.copy()
+    ctx[1] = 69          # more new tokens than context
+    tables[2, 0] = -1    # a block outside the pool
+    q_bits = rows16(b.rng, (int(qs[-1]), 4, 64), "fp16")
+    out = pa.prefill_fp8_block(dev16(q_bits, "fp16"), *upload(caches), dev(tables), dev(ctx), dev(qs), 0.125, 70)
+    assert device_error() == pa.DEVERR_BAD_CONTEXT | pa.DEVERR_BAD_BLOCK
+    got = values(out, "fp16")
+    assert (got[:90] == 0).all()
+    want = fb.paged_prefill(decode_bits(q_bits, "fp16"), *caches, b.tables, b.ctx, qs, 0.125)
+    assert np.abs(got[90:] - want[90:]).max() < 0.02
+    none = pa.prefill_fp8_block(dev16(q_bits, "fp16")[:0], *upload(caches), dev(tables), dev(ctx),
+                                dev(np.zeros(5, np.int32)), 0.125, 0)
+    assert none.shape == (0, 4, 64) and device_error() == 0
+
+
+def test_prefill_largest_f16_values():
+    """f16 values at the type's end: a code that rounds up past 65504 is clamped, not infinite."""
+    b = Batch([20], 2, 1, 64, 16, "fp16", seed=6)
+    b.value[:] = 0x7BFF
+    caches = b.written()
+    assert fb.logical_rows(caches[1], caches[3], b.tables[0], 20).max() == 65536.0
+    q = rows16(b.rng, (20, 2, 64), "fp16")
+    out = pa.prefill_fp8_block(dev16(q, "fp16"), *upload(caches), dev(b.tables), dev(b.ctx),
+                               dev(np.array([0, 20], np.int32)), 0.125, 20)
+    got = values(out, "fp16")
+    # weights rounded to f16 (2^-11) sum to 1 within 2^-11 and fp32 sums: 65504 (1 +- 2^-10), rounded
+    assert device_error() == 0 and np.abs(got - 65504).max() <= 65504 * 2.0 ** -9 and np.isfinite(got).all()
+
+
 # ------------------------------------------------------------------------------ block moves
 
 @pytest.mark.parametrize("hkv,d,B", [(1, 64, 8), (3, 128, 16), (8, 128, 32), (300, 64, 8)])
@@ -276,3 +352,62 @@ def test_swap_out_and_in():
     for t, was in zip(device, saved):
         assert torch.equal(t[[3, 11, 0]], was[[3, 11, 0]]) and t.float().abs().sum(tuple(range(1, t.dim()))).count_nonzero() == 3
     assert device_error() == 0
+
+
+# ------------------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("dtype,B,hkv,d", [("bf16", 16, 2, 128), ("fp16", 8, 3, 64)])
+def test_a_serving_loop(dtype, B, hkv, d):
+    """Prompts, then chunks mixed with single tokens, then decode steps with copy-on-write of a
+    forked sequence: tables and slots, write, attention and block copies, with nothing read back
+    between the calls of a step; every output against the oracle."""
+    rng = np.random.default_rng(B)
+    hq, T, nb, scale = 2 * hkv, 24, 96, 1.0 / np.sqrt(d)
+    steps = [[30, 0, 17], [40, 21, 1], [1, 5, 1], [1, 1, 1], [1, 1, 1]]
+    order = rng.permutation(nb).astype(np.int32)
+    tables, free, cells = np.full((3, T), -1, np.int32), dev(order), [dev([0], np.int32), dev([0], np.int32)]
+    gt = dev(tables)
+    shape = (nb, hkv, B, d)
+    caches = (np.full(shape, 0x7F, np.uint8), np.full(shape, 0x7F, np.uint8),
+              np.full(shape[:2], np.nan, np.float32), np.full(shape[:2], np.nan, np.float32))
+    gpu, ctx, start = upload(caches), np.zeros(3, np.int64), 0
+    slots = torch.empty(80, dtype=torch.int64, device="cuda")
+    for i, new in enumerate(steps):
+        ctx = ctx + new
+        rows = sum(new) + 2  # a padded batch
+        key, value, q = (rows16(rng, (rows, h, d), dtype, 2 if h == hkv else 0) for h in (hkv, hkv, hq))
+        if i == 3:  # the last block of sequence 0 was shared with a fork: a copy takes its place
+            j = (ctx[0] - 2) // B
+            pair = np.array([[tables[0, j], order[-1]]], np.int32)
+            pa.copy_blocks_fp8_block(*gpu, dev(pair))
+            gt[0, j] = int(order[-1])
+            caches = tuple(x.copy() for x in caches[:4])
+            for c in caches:
+                c[pair[0, 1]] = c[pair[0, 0]]
+            tables[0, j] = order[-1]
+        lens, news = dev(ctx, np.int32), dev(new, np.int32)
+        qs, _ = pa.build_step(news, lens, free, cells[i % 2], gt, B, nb, slots, free_next=cells[1 - i % 2])
+        pa.append_fp8_block(dev16(key, dtype), dev16(value, dtype), *gpu, gt, lens, qs)
+        out = pa.prefill_fp8_block(dev16(q, dtype), *gpu, gt, lens, qs, scale, max(new))
+        one = pa.decode_fp8_block(dev16(q[:3], dtype), *gpu, gt, lens, scale) if max(new) == 1 else None
+        tables, ws, wq, start, errs = fb.build_step(new, ctx, order, start, tables, B, nb, 80)
+        caches = fb.append(*caches[:4], key, value, tables, ctx, wq, dtype)
+        assert not errs and not caches[4]
+        assert device_error() == 0
+        np.testing.assert_array_equal(gt.cpu().numpy(), tables)
+        np.testing.assert_array_equal(slots.cpu().numpy(), ws)
+        same(gpu, caches)
+        want = fb.paged_prefill(decode_bits(q, dtype), *caches[:4], tables, ctx, wq, scale)
+        # values reach 2^2 * 4: within the bound of one output, taken at its largest
+        step = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+        for got, row in [(out, None), (one, range(3))]:
+            if got is None:
+                continue
+            got = values(got, dtype)
+            for s in range(3):
+                k = fb.logical_rows(caches[0], caches[2], tables[s], int(ctx[s]))
+                v = fb.logical_rows(caches[1], caches[3], tables[s], int(ctx[s]))
+                for r in range(int(wq[s]), int(wq[s + 1])):
+                    n = int(ctx[s]) - (int(wq[s + 1]) - 1 - r)
+                    most = bound(decode_bits(q[r], dtype), k[:n], v[:n], scale, want[r], dtype, step)
+                    assert (np.abs(got[r] - want[r]) <= most).all(), (i, s, r)
