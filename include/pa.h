@@ -312,7 +312,8 @@ int pa_append_fp8_block(const void* key, const void* value, void* k_cache, void*
  * out are fp16 or bf16 (`dtype`).  The codes are widened to f16 exactly and multiplied on the
  * tensor cores in f16 (bf16 queries rounded to f16, so |q| < 65520); the K scale multiplies
  * the fp32 scores, the V scale the softmax weights before they are rounded to f16, relative
- * to the largest V scale met so far, so that its size does not matter; accumulation fp32.
+ * to the largest V scale met so far, so that its size does not matter; accumulation fp32;
+ * outputs past the type's largest value are clamped to it (a cached 65504 is held as 65536).
  * Same workspace, ordering, error and determinism rules as pa_decode. */
 int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                         const float* k_scales, const float* v_scales, const int32_t* block_tables,
@@ -320,18 +321,21 @@ int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                         int num_blocks, float scale, void* out, void* workspace,
                         size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream);
-/* pa_prefill over those blocks: the arguments and rules of pa_prefill, K and V the values
- * decode(code) * scale of each token's block.  The kernel widens them to `dtype`: exactly
- * where the scale is a power of two and the value lies in the type's range, else rounded to
- * nearest-even, magnitudes above its largest value clamped to it.  Write the sequences'
- * new tokens first (pa_append_fp8_block). */
+/* pa_prefill over those blocks: the arguments and rules of pa_prefill with K and V the values
+ * decode(code) * scale of each token's block, and two more: num_tokens, the rows of q and out
+ * (a sequence whose span lies outside them gets PA_DEVERR_BAD_CONTEXT and nothing is read
+ * or written for it; rows behind the last sequence are not touched), and scale > 0.
+ * Products run in f16: codes are widened relative to the largest scale near them, bf16 rows
+ * of q brought to the type's upper range by a power of two, softmax weights rounded to f16;
+ * accumulation fp32; outputs clamped as by pa_decode_fp8_block.  Write the sequences' new
+ * tokens first (pa_append_fp8_block). */
 int pa_prefill_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                          const float* k_scales, const float* v_scales,
                          const int32_t* block_tables, int max_blocks_per_seq,
                          const int32_t* context_lens, const int32_t* query_start, int num_seqs,
-                         int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
-                         int block_size, int num_blocks, float scale, void* out, pa_dtype dtype,
-                         cudaStream_t stream);
+                         int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
+                         int head_dim, int block_size, int num_blocks, float scale, void* out,
+                         pa_dtype dtype, cudaStream_t stream);
 /* pa_copy_blocks for those blocks: codes and scales of each pair, in one launch. */
 int pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
                              const int32_t* block_mapping, int num_pairs, int num_blocks,

@@ -77,7 +77,7 @@ SIGNATURES = {
     "pa_decode_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _vp, _vp, _sz, _i32, _vp]),
     "pa_prefill_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
-                                    _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp]),
+                                    _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp]),
     "pa_copy_blocks_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                         _vp]),
     "pa_swap_blocks_fp8_block": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
@@ -827,8 +827,8 @@ def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, con
     _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     args = (_dev(q, "q"), kc, vc, ks, vs, _dev(block_tables, "block_tables", torch.int32),
             block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32),
-            _dev(query_start, "query_start", torch.int32), n, int(max_query_len), hq, hkv, d, bs,
-            nb, float(scale), _dev(out, "out"), _dtype_code(q))
+            _dev(query_start, "query_start", torch.int32), n, ntok, int(max_query_len), hq, hkv, d,
+            bs, nb, float(scale), _dev(out, "out"), _dtype_code(q))
     if plan:
         return Launch("pa_prefill_fp8_block", args, out,
                       keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,

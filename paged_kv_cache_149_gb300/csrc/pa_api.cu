@@ -476,7 +476,8 @@ int prefill_call(const void* q, const void* k_cache, const void* v_cache, const 
                  const int32_t* context_lens, const int32_t* query_start, int num_seqs,
                  int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
                  int block_size, int num_blocks, float scale, void* out, pa_dtype dtype,
-                 cudaStream_t stream) {
+                 cudaStream_t stream, int num_tokens = 0) {
+  const bool fp8_block = k_scales != nullptr;
   if (num_seqs < 0 || max_query_len < 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
       !shape_ok(num_kv_heads, head_dim, block_size) || num_q_heads < num_kv_heads ||
       num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > 64 ||
@@ -510,9 +511,8 @@ int prefill_call(const void* q, const void* k_cache, const void* v_cache, const 
   a.scale = scale;
   a.bf16 = dtype == PA_BF16;
   a.err = di.err;
-  a.k_scales = k_scales;
-  a.v_scales = v_scales;
-  return pa::prefill_launch(a, stream);
+  return fp8_block ? pa::prefill_fp8_block_launch(a, num_tokens, k_scales, v_scales, stream)
+                   : pa::prefill_launch(a, stream);
 }
 
 }  // namespace
@@ -532,15 +532,18 @@ int pa_prefill_fp8_block(const void* q, const void* k_cache, const void* v_cache
                          const float* k_scales, const float* v_scales,
                          const int32_t* block_tables, int max_blocks_per_seq,
                          const int32_t* context_lens, const int32_t* query_start, int num_seqs,
-                         int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
-                         int block_size, int num_blocks, float scale, void* out, pa_dtype dtype,
-                         cudaStream_t stream) {
+                         int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
+                         int head_dim, int block_size, int num_blocks, float scale, void* out,
+                         pa_dtype dtype, cudaStream_t stream) {
+  if (num_tokens < 0 || !(scale > 0.f)) return PA_ERR_ARG;
+  if (num_tokens < max_query_len) max_query_len = num_tokens;  // (no sequence has more rows)
   if (num_seqs > 0 && max_query_len > 0 &&
       !fp8_block_arrays_ok(k_cache, v_cache, k_scales, v_scales))
     return PA_ERR_ARG;
   return prefill_call(q, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks_per_seq,
                       context_lens, query_start, num_seqs, max_query_len, num_q_heads,
-                      num_kv_heads, head_dim, block_size, num_blocks, scale, out, dtype, stream);
+                      num_kv_heads, head_dim, block_size, num_blocks, scale, out, dtype, stream,
+                      num_tokens);
 }
 
 int pa_decode_append(const void* q, const void* key_new, const void* value_new, void* k_cache,

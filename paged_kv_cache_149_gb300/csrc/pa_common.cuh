@@ -173,6 +173,24 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// The same with magnitudes above the type's largest (infinities too) clamped to it.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_sat(float a, float b);
+
+template <>
+__device__ __forceinline__ uint32_t pack2_sat<__nv_bfloat16>(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+template <>
+__device__ __forceinline__ uint32_t pack2_sat<__half>(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 // One float -> one 16-bit value, round to nearest even.
 template <typename T>
 __device__ __forceinline__ T from_float(float v);

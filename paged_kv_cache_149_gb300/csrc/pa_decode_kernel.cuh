@@ -511,6 +511,14 @@ __device__ __forceinline__ int arrive(unsigned long long* ctr, unsigned long lon
   return arrive_count(ctr, epoch, n, DeviceCas(), DeviceLoad());
 }
 
+// Two output values of a K/V format.  With block scales a cached value may round up past f16's
+// largest (65504 is held as 65536), and an average of such values with it: it is clamped.
+template <typename T, int KV>
+__device__ __forceinline__ uint32_t pack_out(float a, float b) {
+  if constexpr (KV == kKvFp8Block) return pack2_sat<T>(a, b);
+  else return pack2<T>(a, b);
+}
+
 // Merge the pieces of a cut pair held by CTAs c..c_last (c's piece in slot `first_slot`,
 // the others in slot 0), pieces taken in CTA order so the result is deterministic:
 //   M = max m_i,  w_i = 2^(m_i - M) (0 for an empty piece),  L = sum l_i w_i,
@@ -518,7 +526,7 @@ __device__ __forceinline__ int arrive(unsigned long long* ctr, unsigned long lon
 // (the log-sum-exp rescaling of online softmax); zeros when a piece saw a bad block.
 // merge_staged computes the same sums in the same order with the same fused multiply-adds,
 // so a pair's output does not depend on which of the two merges it.
-template <int D, typename T, bool QK>
+template <int D, typename T, int KV>
 __device__ void merge_pieces(const Params& p, int pi, int c, int first_slot, int c_last, int nh,
                              T* out_rows, int gt, int gthreads) {
   constexpr int C4 = D / 4;  // 4-float chunks per head row
@@ -552,9 +560,9 @@ __device__ void merge_pieces(const Params& p, int pi, int c, int first_slot, int
     }
     uint2 packed = make_uint2(0u, 0u);
     if (!bad) {
-      const float inv = QK ? p.out_scale / L : 1.f / L;
-      packed.x = pack2<T>(O.x * inv, O.y * inv);
-      packed.y = pack2<T>(O.z * inv, O.w * inv);
+      const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
+      packed.x = pack_out<T, KV>(O.x * inv, O.y * inv);
+      packed.y = pack_out<T, KV>(O.z * inv, O.w * inv);
     }
     *reinterpret_cast<uint2*>(out_rows + h * D + d4) = packed;
   }
@@ -573,7 +581,7 @@ __device__ __forceinline__ bool mbar_wait_limit(uint32_t bar, uint32_t parity) {
 
 // merge_staged when every piece of both pairs fits in the ring at once: every piece's O
 // by one bulk copy, the (m, l) by plain loads behind them, a single round trip.
-template <int D, typename T, bool QK>
+template <int D, typename T, int KV>
 __device__ bool merge_staged_once(const Params& p, int pi, const CutPiece& job0,
                                   const CutPiece& job1, int njobs, uint32_t ring,
                                   uint8_t* ring_ptr, uint32_t bar, uint32_t& bar_phase, int lane) {
@@ -670,9 +678,9 @@ __device__ bool merge_staged_once(const Params& p, int pi, const CutPiece& job0,
       const float L = ml[moff + h].y;
       uint2 packed = make_uint2(0u, 0u);
       if (L >= 0.f) {
-        const float inv = QK ? p.out_scale / L : 1.f / L;
-        packed.x = pack2<T>(O.x * inv, O.y * inv);
-        packed.y = pack2<T>(O.z * inv, O.w * inv);
+        const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
+        packed.x = pack_out<T, KV>(O.x * inv, O.y * inv);
+        packed.y = pack_out<T, KV>(O.z * inv, O.w * inv);
       }
       *reinterpret_cast<uint2*>(out_rows + h * D + d4) = packed;
     }
@@ -692,13 +700,13 @@ __device__ bool merge_staged_once(const Params& p, int pi, const CutPiece& job0,
 // with the same fused multiply-adds as merge_pieces, so a pair's output does not depend on
 // which CTA merges it.  Returns false, having done nothing, when the (m, l) of the pieces
 // do not fit in half the ring (a pair cut into thousands of pieces): merge_pieces then.
-template <int D, typename T, bool QK>
+template <int D, typename T, int KV>
 __device__ bool merge_staged_chunked(const Params& p, int pi, const CutPiece& job0,
                                      const CutPiece& job1, int njobs, uint32_t ring,
                                      uint8_t* ring_ptr, int ring_bytes, uint32_t bar,
                                      uint32_t& bar_phase, int lane);
 
-template <int D, typename T, bool QK>
+template <int D, typename T, int KV>
 __device__ __forceinline__ bool merge_staged(const Params& p, int pi, const CutPiece& job0,
                                              const CutPiece& job1, int njobs, uint32_t ring,
                                              uint8_t* ring_ptr, int ring_bytes, uint32_t bar,
@@ -713,13 +721,13 @@ __device__ __forceinline__ bool merge_staged(const Params& p, int pi, const CutP
   const int np1 = njobs > 1 ? job1.c_last - job1.c_first + 1 : 0;
   const uint32_t acc_bytes = np0 * job0.nh * D * 4 + np1 * job1.nh * D * 4;
   if (acc_bytes + ml_bytes <= static_cast<uint32_t>(ring_bytes))
-    return merge_staged_once<D, T, QK>(p, pi, job0, job1, njobs, ring, ring_ptr, bar, bar_phase,
+    return merge_staged_once<D, T, KV>(p, pi, job0, job1, njobs, ring, ring_ptr, bar, bar_phase,
                                        lane);
-  return merge_staged_chunked<D, T, QK>(p, pi, job0, job1, njobs, ring, ring_ptr, ring_bytes, bar,
+  return merge_staged_chunked<D, T, KV>(p, pi, job0, job1, njobs, ring, ring_ptr, ring_bytes, bar,
                                         bar_phase, lane);
 }
 
-template <int D, typename T, bool QK>
+template <int D, typename T, int KV>
 __device__ bool merge_staged_chunked(const Params& p, int pi, const CutPiece& job0,
                                      const CutPiece& job1, int njobs, uint32_t ring,
                                      uint8_t* ring_ptr, int ring_bytes, uint32_t bar,
@@ -841,9 +849,9 @@ __device__ bool merge_staged_chunked(const Params& p, int pi, const CutPiece& jo
       const float L = ml[moff + h].y;
       uint2 packed = make_uint2(0u, 0u);
       if (L >= 0.f) {
-        const float inv = QK ? p.out_scale / L : 1.f / L;
-        packed.x = pack2<T>(O[it].x * inv, O[it].y * inv);
-        packed.y = pack2<T>(O[it].z * inv, O[it].w * inv);
+        const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
+        packed.x = pack_out<T, KV>(O[it].x * inv, O[it].y * inv);
+        packed.y = pack_out<T, KV>(O[it].z * inv, O[it].w * inv);
       }
       *reinterpret_cast<uint2*>(out_rows + h * D + d4) = packed;
     }
@@ -1849,7 +1857,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
                 *reinterpret_cast<uint32_t*>(out_rows + h * D + drow<D, QK>(mt, r0)) =
-                    pack2<T>(o[mt][nt][cc] * inv, o[mt][nt][cc + 2] * inv);
+                    pack_out<T, KV>(o[mt][nt][cc] * inv, o[mt][nt][cc + 2] * inv);
             }
           }
       } else {
@@ -1927,9 +1935,9 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
         if (whole) {
           uint2 packed = make_uint2(0u, 0u);  // zeros for a pair with a bad block
           if (!any_bad) {
-            const float inv = QK ? p.out_scale / L : 1.f / L;
-            packed.x = pack2<T>(acc.x * inv, acc.y * inv);
-            packed.y = pack2<T>(acc.z * inv, acc.w * inv);
+            const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
+            packed.x = pack_out<T, KV>(acc.x * inv, acc.y * inv);
+            packed.y = pack_out<T, KV>(acc.z * inv, acc.w * inv);
           }
           *reinterpret_cast<uint2*>(out_rows + h * D + d4) = packed;
         } else {
@@ -1992,7 +2000,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       const int nj = (bits & 1) + ((bits >> 1) & 1);
       const CutPiece& j0 = (bits & 1) ? cut_a : cut_b;
       uint32_t phase = 0;
-      if (merge_staged<D, T, QK>(p, pi, j0, cut_b, nj, ring, sm.ring[warp][0], R * G_::kStageBytes,
+      if (merge_staged<D, T, KV>(p, pi, j0, cut_b, nj, ring, sm.ring[warp][0], R * G_::kStageBytes,
                                  smem_addr(&sm.merge_bar[warp]), phase, lane))
         bits = 0;
     }
@@ -2001,7 +2009,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       const CutPiece& cp = k == 0 ? cut_a : cut_b;
       T* out_rows =
           reinterpret_cast<T*>(p.out) + (static_cast<size_t>(cp.s) * p.num_q_heads + cp.h0) * D;
-      merge_pieces<D, T, QK>(p, pi, cp.c_first, cp.first_slot, cp.c_last, cp.nh, out_rows, gt,
+      merge_pieces<D, T, KV>(p, pi, cp.c_first, cp.first_slot, cp.c_last, cp.nh, out_rows, gt,
                          gthreads);
     }
   }

@@ -54,12 +54,16 @@ struct PrefillArgs {
   float scale;
   bool bf16;
   unsigned* err;
-  const float* k_scales = nullptr;  // FP8 blocks with block scales: [NB][Hkv]
-  const float* v_scales = nullptr;
 };
 
 // Launch the paged prefill kernel; 0 or a negative PA_ERR_* code.
 int prefill_launch(const PrefillArgs& a, cudaStream_t stream);
+// The same over FP8 blocks with block scales [NB][Hkv]; q has num_tokens rows.
+int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* k_scales,
+                             const float* v_scales, cudaStream_t stream);
+// q as [tokens][Hq][d] 16-bit for TMA loads of whole 128-row query tiles; false when the
+// group does not divide 128 or the driver's encoder is missing or rejects the tensor.
+bool q_tile_map(CUtensorMap* map, const void* q, int hq, int d, int g, long long tokens);
 
 int reshape_and_cache_launch(const void* key, const void* value, void* k_cache, void* v_cache,
                              const int64_t* slot_mapping, int num_tokens, int num_blocks,

@@ -56,9 +56,12 @@
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 namespace prefill {
+
+using namespace tc;
 
 constexpr int kTiles = 2;       // query tiles per CTA (softmax warpgroups)
 constexpr int kRows = 128;      // rows of a query tile (MMA M, tensor-memory lanes)
@@ -68,17 +71,7 @@ constexpr int kTableAhead = 4;  // tiles the loader looks block-table entries up
 constexpr int kLoadWarp = 8;    // loads Q and the K tiles
 constexpr int kLoadWarpV = 11;  // loads the V tiles
 constexpr int kMmaWarp = 9;     // MMA issue for tile 0; tile 1 has the next warp
-// 2 x 128 softmax threads, two loader warps, two MMA warps; over FP8 blocks a fourth
-// warpgroup that widens codes (then the loader warps load Q alone)
-template <bool KV8>
-constexpr int kThreadsOf = KV8 ? 512 : 384;
-constexpr int kWidenWarp = 12;  // the first of kWidenWarps
-constexpr int kWidenWarps = 4;
-// Registers over FP8 blocks: 512 threads launch with 128 each; the softmax warpgroups, which
-// hold a row of scores, take 160 and the other two keep 96 (2 x 160 + 2 x 96 = 4 x 128;
-// 168 + 88 and 152 + 104 make one side spill).
-constexpr int kSoftmaxRegs = 160;
-constexpr int kOtherRegs = 96;
+constexpr int kThreads = 384;   // 2 x 128 softmax threads, two loader warps, two MMA warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that forces a rescale of O
 
@@ -99,8 +92,6 @@ struct Params {
   int ncb;  // query blocks (of kTiles x tpt tokens) of the longest sequence
   float scale_log2;
   unsigned* err;
-  const float* k_scales;  // FP8 blocks: [num_blocks][Hkv], else null
-  const float* v_scales;
 };
 
 template <int D>
@@ -119,184 +110,8 @@ struct Smem {
   int abort;  // a wait gave up: every role stops
 };
 
-// Byte offset of (row, 16-byte chunk) in a [rows][D] 16-bit tile stored K-major with the
-// 128-byte swizzle: chunk c lives in the 64-element column block c / 8 (blocks rows * 128
-// bytes apart), row r at r * 128 inside it, the chunk index XORed with r % 8.  TMA with
-// the 128-byte swizzle writes the same pattern into a 1024-byte aligned box.
-__device__ __forceinline__ uint32_t swz(int rows, int r, int c) {
-  return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-// tcgen05 shared-memory matrix descriptor with the 128-byte swizzle (version 1 = sm_100
-// family): lbo / sbo in bytes.  K-major operands: sbo = 1024 (8-row groups), lbo unused.
-// MN-major operands: lbo = distance between 64-element MN blocks, sbo = 1024.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) |
-         (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// tcgen05 instruction descriptor, kind::f16: fp32 accumulate, A and B of the same 16-bit
-// type (bf16 or fp16), A K-major, B K-major or MN-major, M, N.
-template <typename T>
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((std::is_same<T, __nv_bfloat16>::value ? 1u : 0u) << 7) |
-         ((std::is_same<T, __nv_bfloat16>::value ? 1u : 0u) << 10) |
-         ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc,
-                                        bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(da), "l"(db), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// 32 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16 columns (32 packed 16-bit values) written to this thread's lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
-// tcgen05.mma with A from tensor memory (lane = row, column c = elements 2c and 2c + 1).
-__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db,
-                                           uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(db), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
-}
-
-// The same 32 columns written back.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
-          taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
-      "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
-      "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-      "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
-      "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
-      "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
-      : "memory");
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(src_bytes)
-               : "memory");
-}
-// One arrival on `bar` once every cp.async this thread has issued so far has landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// 2^x by the special-function unit (approximate, subnormal results flushed to zero; the
-// arguments here are <= 8 and results below 2^-126 only lose weights that small).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// max(a, b, c) in one instruction.
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// 3-D tiled TMA load through the tensor map at `map` (a kernel parameter); completion
-// counted in bytes on `bar`.  x * the element size is a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-// Two values of a type in one word, magnitudes above its largest clamped to it.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2_sat(float2 v) {
-  uint32_t r;
-  if constexpr (std::is_same<T, __nv_bfloat16>::value)
-    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
-  else
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
-  return r;
-}
-
-// Eight codes (two words) times a scale -> eight 16-bit values.
-template <typename T>
-__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, float scale) {
-  const float2 s2 = make_float2(scale, scale);
-  uint4 w;
-  w.x = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(lo)), s2));
-  w.y = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(lo >> 16)), s2));
-  w.z = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(hi)), s2));
-  w.w = pack2_sat<T>(__fmul2_rn(e4m3x2_floats(static_cast<uint16_t>(hi >> 16)), s2));
-  return w;
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-
-// KV8: the caches hold FP8 (E4M3) codes with a scale per (block, kv head).  Four warps widen
-// them to 16-bit tiles in shared memory; the rest of the kernel is the same.
-template <int D, typename T, bool KV8>
-__global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __grid_constant__ Params p) {
-  constexpr int kThreads = kThreadsOf<KV8>;
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p) {
   constexpr int CH = D / 8;                  // 16-byte chunks of a 16-bit row
   constexpr int KS1 = D / 16;                // MMA k-steps of S = Q K^T
   constexpr int KS2 = kKeys / 16;            // MMA k-steps of P V
@@ -351,8 +166,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __gri
   if (tid == 0) {
     mbar_init(smem_addr(&sm.q_full), 33);  // TMA expect-tx + 32 copy lanes
     for (int i = 0; i < kStages; ++i) {
-      // per loader: TMA expect-tx + 32 copy lanes; KV8: every lane that widens
-      mbar_init(smem_addr(&sm.kv_full[i]), KV8 ? 32 * kWidenWarps : 66);
+      mbar_init(smem_addr(&sm.kv_full[i]), 66);  // per loader: TMA expect-tx + 32 copy lanes
     }
     for (int t = 0; t < kTiles; ++t)
       for (int b = 0; b < 2; ++b) {
@@ -383,15 +197,13 @@ __global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __gri
     return false;
   };
 
-  if (warp >= kLoadWarp) {
-  if constexpr (KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kLoadWarp || warp >= kLoadWarpV) {
+  if (warp == kLoadWarp || warp == kLoadWarpV) {
     // ===== loaders: Q once (the K loader), then the K (or V) tiles of the ring =====
     // Two warps, because one thread issuing TMA copies moves only about 26 GB/s per SM:
     // with one loader a 64-key step of both query tiles (32 KB of K and V) took about 2200
     // cycles to issue, against about 1300 cycles of tensor work.
     const bool is_v = warp == kLoadWarpV;
-    if (warp == kLoadWarp) {
+    if (!is_v) {
       // Q of both tiles: a whole tile (tpt tokens x G heads = 128 rows, each token's G rows
       // contiguous in q) by TMA, one copy per 64-column half; a tile that runs past the
       // sequence by 16-byte copies, zero-filled past its last token (token-major, no
@@ -430,79 +242,6 @@ __global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __gri
       }
       cp_async_arrive(smem_addr(&sm.q_full));
     }
-    if constexpr (KV8) {
-      if (warp >= kWidenWarp) {
-      // FP8 blocks: widening warp cw takes rows 16 cw .. 16 cw + 15 of every K and V tile
-      // (two groups of eight rows; eight rows never straddle a block).  A lane holds 16 codes
-      // of a row per load; the codes and scales of the next tile are fetched into the same
-      // registers as soon as this tile's are widened, its table entries a tile earlier.  Each code becomes
-      // the 16-bit value code * scale (exact for a power of two inside the type's range,
-      // otherwise rounded, and clamped to the type's largest), so the tiles, the MMAs and the
-      // softmax are those of 16-bit blocks.
-      constexpr int CPR = D / 16;    // 16-code chunks of a row
-      constexpr int RPI = 32 / CPR;  // rows a warp fetches at once
-      constexpr int NI = 16 / RPI;
-      const int cw = warp - kWidenWarp;
-      const int col = lane % CPR, rsub = lane / CPR;
-      const int log2b = 31 - __clz(p.block_size);
-      const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-      auto entry = [&](int kt, int grp) -> int {  // -1 past the keys or the context
-        const int pos = kt * kKeys + 16 * cw + 8 * grp;
-        return kt < n && pos < ctx ? __ldg(trow + (pos >> log2b)) : -1;
-      };
-      // this warp's codes of a tile of one cache, and its two groups' scales
-      auto fetch = [&](const uint8_t* cache, const float* scales, int kt, const int (&e)[2],
-                       uint4 (&c)[NI], float (&sc)[2]) {
-        const int pos0 = kt * kKeys + 16 * cw;
-#pragma unroll
-        for (int grp = 0; grp < 2; ++grp) {
-          const bool used = kt < n && pos0 + 8 * grp < ctx;
-          const bool ok = used && e[grp] >= 0 && e[grp] < p.num_blocks;
-          if (used && !ok && lane == 0) sm.bad = 1;
-          const size_t group = static_cast<size_t>(ok ? e[grp] : 0) * p.num_kv_heads + g;
-          sc[grp] = ok ? __ldg(scales + group) : 0.f;
-#pragma unroll
-          for (int i = grp * NI / 2; i < (grp + 1) * NI / 2; ++i) {
-            const int pos = pos0 + i * RPI + rsub;
-            const size_t at = ((group << log2b) + (pos & (p.block_size - 1))) * D + col * 16;
-            c[i] = ok && pos < ctx ? __ldg(reinterpret_cast<const uint4*>(cache + at)) : make_uint4(0, 0, 0, 0);
-          }
-        }
-      };
-      // 16 values as two 16-byte chunks of the tile's row; lanes of the right 64-column half
-      // store the odd chunk first, so the eight lanes of a row meet eight bank groups
-      auto put = [&](uint32_t tile, int row, const uint4& c, float scale) {
-        const uint4 a = widen8<T>(c.x, c.y, scale), b = widen8<T>(c.z, c.w, scale);
-        const bool odd = 2 * col >= 8;
-        st_shared16(tile + swz(kKeys, row, 2 * col + (odd ? 1 : 0)), odd ? b : a);
-        st_shared16(tile + swz(kKeys, row, 2 * col + (odd ? 0 : 1)), odd ? a : b);
-      };
-      uint4 ck[NI], cv[NI];
-      float sk[2], sv[2];
-      int e[2] = {entry(0, 0), entry(0, 1)};
-      fetch(p.k_cache, p.k_scales, 0, e, ck, sk);
-      fetch(p.v_cache, p.v_scales, 0, e, cv, sv);
-      e[0] = entry(1, 0);
-      e[1] = entry(1, 1);
-      for (int kt = 0; kt < n; ++kt) {
-        const int st = kt % kStages;
-        if (kt >= kStages && !(wait(sm.o_done[0][st], ((kt - kStages) / kStages) & 1) &&
-                               wait(sm.o_done[1][st], ((kt - kStages) / kStages) & 1)))
-          break;
-        const uint32_t kb = smem_addr(sm.k[st]), vb = smem_addr(sm.v[st]);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) put(kb, 16 * cw + i * RPI + rsub, ck[i], sk[i * RPI / 8]);
-        fetch(p.k_cache, p.k_scales, kt + 1, e, ck, sk);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) put(vb, 16 * cw + i * RPI + rsub, cv[i], sv[i * RPI / 8]);
-        fetch(p.v_cache, p.v_scales, kt + 1, e, cv, sv);
-        e[0] = entry(kt + 2, 0);
-        e[1] = entry(kt + 2, 1);
-        fence_async_smem();  // these stores before the tensor cores' reads
-        mbar_arrive(smem_addr(&sm.kv_full[st]));
-      }
-      }
-    } else {
     const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
     const CUtensorMap* tmap = is_v ? &p.vmap : &p.kmap;
     const int B = p.block_size, nbk = kKeys / B;
@@ -565,9 +304,8 @@ __global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __gri
       }
       cp_async_arrive(smem_addr(&sm.kv_full[st]));
     }
-    }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ============ MMA issue: one thread per query tile (issue cost is per thread) ============
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16<T>(kRows, kKeys, false);
@@ -635,9 +373,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __gri
       wait(sm.fin, 0);
     }
     __syncwarp();
-  }
   } else {
-    if constexpr (KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ================= softmax: warpgroup t, one thread per row =================
     const int t = warp >> 2, r = tid & (kRows - 1);
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + t * kTileCols;
@@ -802,10 +538,10 @@ __global__ void __launch_bounds__(kThreadsOf<KV8>, 1) prefill_kernel(const __gri
   }
 }
 
-template <int D, typename T, bool KV8>
+template <int D, typename T>
 int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<D>) + 1024;
-  auto* kern = prefill_kernel<D, T, KV8>;
+  auto* kern = prefill_kernel<D, T>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return -3;
   cudaLaunchConfig_t cfg = {};
   const int per_cta = kTiles * prm.tpt;
@@ -815,7 +551,7 @@ int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
   // x: a block within its half (the later half has ceil(ncb / 2)), y: sequence,
   // z: half x kv head
   cfg.gridDim = dim3((ncb + 1) / 2, prm.num_seqs, 2 * prm.num_kv_heads);
-  cfg.blockDim = dim3(kThreadsOf<KV8>);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -870,9 +606,9 @@ bool kv_cache_map(CUtensorMap* map, const void* base, int elem_bytes, int num_bl
 }
 
 // q as [tokens][Hq][d] 16-bit with a box of one query tile's 64-column half: (64, G,
-// 128 / G).  `tokens` bounds the rows a launch may read (num_seqs x max_query_len); only
-// tiles that lie wholly inside their sequence are read through it.
-static bool q_map(CUtensorMap* map, const void* q, int hq, int d, int g, long long tokens) {
+// 128 / G).  `tokens` bounds the rows a launch may read (here num_seqs x max_query_len);
+// only tiles that lie wholly inside their sequence are read through it.
+bool q_tile_map(CUtensorMap* map, const void* q, int hq, int d, int g, long long tokens) {
   EncodeTiledFn fn = encode_tiled();
   if (!fn || prefill::kRows % g != 0 || tokens < 1) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hq),
@@ -887,14 +623,11 @@ static bool q_map(CUtensorMap* map, const void* q, int hq, int d, int g, long lo
 
 int prefill_launch(const PrefillArgs& a, cudaStream_t stream) {
   prefill::Params p;
-  const bool kv8 = a.k_scales != nullptr;
-  if (!kv8 && (!kv_cache_map(&p.kmap, a.k_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
-                             a.head_dim) ||
-               !kv_cache_map(&p.vmap, a.v_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
-                             a.head_dim)))
+  if (!kv_cache_map(&p.kmap, a.k_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
+                    a.head_dim) ||
+      !kv_cache_map(&p.vmap, a.v_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size,
+                    a.head_dim))
     return -3;
-  p.k_scales = a.k_scales;
-  p.v_scales = a.v_scales;
   p.q = static_cast<const uint8_t*>(a.q);
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);
   p.v_cache = static_cast<const uint8_t*>(a.v_cache);
@@ -911,19 +644,16 @@ int prefill_launch(const PrefillArgs& a, cudaStream_t stream) {
   p.block_size = a.block_size;
   p.num_blocks = a.num_blocks;
   p.scale_log2 = a.scale * prefill::kLog2e;
-  p.q_tma = q_map(&p.qmap, a.q, a.num_q_heads, a.head_dim, p.group,
+  p.q_tma = q_tile_map(&p.qmap, a.q, a.num_q_heads, a.head_dim, p.group,
                   static_cast<long long>(a.num_seqs) * a.max_query_len)
                 ? 1 : 0;
   p.err = a.err;
-#define PA_PREFILL_CASE(DD, K8)                                                         \
-  if (a.head_dim == DD && kv8 == K8)                                                    \
-    return a.bf16 ? prefill::launch<DD, __nv_bfloat16, K8>(p, a.max_query_len, stream)  \
-                  : prefill::launch<DD, __half, K8>(p, a.max_query_len, stream);
-  PA_PREFILL_CASE(128, false)
-  PA_PREFILL_CASE(64, false)
-  PA_PREFILL_CASE(128, true)
-  PA_PREFILL_CASE(64, true)
-#undef PA_PREFILL_CASE
+  if (a.head_dim == 128)
+    return a.bf16 ? prefill::launch<128, __nv_bfloat16>(p, a.max_query_len, stream)
+                  : prefill::launch<128, __half>(p, a.max_query_len, stream);
+  if (a.head_dim == 64)
+    return a.bf16 ? prefill::launch<64, __nv_bfloat16>(p, a.max_query_len, stream)
+                  : prefill::launch<64, __half>(p, a.max_query_len, stream);
   return -1;
 }
 

@@ -64,9 +64,10 @@ def test_decode_refusals(libpa, bad):
     assert libpa.lib().pa_decode_fp8_block(*decode_args(**bad)) == libpa.PA_ERR_ARG
 
 
-@pytest.mark.parametrize("bad", BAD_ATTENTION + [dict(most=-1), dict(qs=None), dict(hq=130)])
+@pytest.mark.parametrize("bad", BAD_ATTENTION + [dict(most=-1), dict(rows=-1), dict(qs=None),
+                                                 dict(hq=130), dict(scale=0.0), dict(scale=-0.1)])
 def test_prefill_refusals(libpa, bad):
-    a = dict(q=P, kc=P, vc=P, ks=P, vs=P, tables=P, T=T, c=P, qs=P, n=N, most=9, hq=HQ, hkv=HKV, d=D,
+    a = dict(q=P, kc=P, vc=P, ks=P, vs=P, tables=P, T=T, c=P, qs=P, n=N, rows=20, most=9, hq=HQ, hkv=HKV, d=D,
              B=B, nb=NB, scale=0.1, out=P, dtype=1)
     a.update(bad)
     assert libpa.lib().pa_prefill_fp8_block(*a.values(), None) == libpa.PA_ERR_ARG

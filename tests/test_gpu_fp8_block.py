@@ -313,6 +313,11 @@ def test_prefill_largest_f16_values():
     got = values(out, "fp16")
     # weights rounded to f16 (2^-11) sum to 1 within 2^-11 and fp32 sums: 65504 (1 +- 2^-10), rounded
     assert device_error() == 0 and np.abs(got - 65504).max() <= 65504 * 2.0 ** -9 and np.isfinite(got).all()
+    for ctx in (20, 2000):  # and decode's, whole and cut between SMs
+        b = Batch([ctx], 2, 1, 64, 16, "fp16", seed=6)
+        b.value[:] = 0x7BFF
+        got = values(pa.decode_fp8_block(dev16(q[:1], "fp16"), *upload(b.written()), dev(b.tables), dev(b.ctx), 0.125), "fp16")
+        assert device_error() == 0 and np.abs(got - 65504).max() <= 65504 * 2.0 ** -9 and np.isfinite(got).all()
 
 
 # ------------------------------------------------------------------------------ block moves
