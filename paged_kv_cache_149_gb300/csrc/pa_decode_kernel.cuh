@@ -875,9 +875,9 @@ struct Smem {
   // quantised blocks, fused step: the newest token's 16-bit K and V rows, per ring slot
   uint8_t newrow[kWarps][Geo<D, KV>::kSlots][KV == kKv16 || KV == kKvFp8Block ? 16 : 4 * D];
   // FP8 blocks with block scales, per ring slot: the K scales of the stage's four groups of
-  // eight tokens, then their V scales
-  float bscale[KV == kKvFp8Block ? kWarps : 1][Geo<D, KV>::kSlots][KV == kKvFp8Block ? 8 : 1];
-  float xo[kWarps][4][D];  // per-warp O rows, 4 heads per exchange round
+  // eight tokens, then their V scales (read as float4, as xo is)
+  alignas(16) float bscale[KV == kKvFp8Block ? kWarps : 1][Geo<D, KV>::kSlots][KV == kKvFp8Block ? 8 : 4];
+  alignas(16) float xo[kWarps][4][D];  // per-warp O rows, 4 heads per exchange round
   float xm[kWarps][kMaxHeads], xl[kWarps][kMaxHeads];
   long long scan[kWarps];
   long long start_pre;

@@ -18,7 +18,12 @@
 // that are powers of two no step rounds but those of values 2^-15 and more below their
 // reference (an absolute 2^-25 of it); other scales round each widened value once.
 //
-// Design: one CTA per (pair of 128-row query tiles, sequence, kv head), 640 threads:
+// Design: persistent CTAs of 640 threads, one per SM; a work item is a (pair of 128-row query
+// tiles, sequence, kv head).  The grid has a CTA per item; a running CTA claims items of CTAs
+// that have not started (cluster launch control), so the SMs balance themselves, and its roles
+// go from item to item at their own pace: the next item's codes, K, V and q arrive while this
+// one's last tiles are multiplied and written out.  (One CTA per item spent about 13600 cycles
+// of its 34000, 8 prompts of 2048 tokens, on starting up and writing out alone.)
 // * A query tile's rows are (token, query head of the kv head) pairs, 128 / G tokens x G
 //   heads; both tiles of the CTA share the key tiles (64 keys each).
 // * Two producer warps (K, V) look blocks and scales up a tile ahead and copy whole blocks of
@@ -37,6 +42,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -52,10 +58,11 @@ using namespace tc;
 constexpr int kTiles = 2;    // query tiles per CTA (softmax warpgroups)
 constexpr int kRows = 128;   // rows of a query tile (MMA M, tensor-memory lanes)
 constexpr int kKeys = 64;    // keys of a K/V tile (MMA N of S, K of P V)
-constexpr int kStages = 4;   // K ring, V ring
+constexpr int kStages = 3;   // K ring, V ring
 constexpr int kGroups = kKeys / 8;  // groups of eight tokens, each inside one block
-constexpr int kMmaWarp = 8;         // MMA issue for query tile 0 (and loads Q); tile 1 has the next
-constexpr int kCodeWarp = 10;       // looks blocks up, copies K codes; the next warp V's
+constexpr int kMmaWarp = 8;         // MMA issue for query tile 0; tile 1 has the next
+constexpr int kItems = 4;           // work items in flight between the roles
+constexpr int kCodeWarp = 10;       // claims items, looks blocks up, copies K codes; the next V's
 constexpr int kWidenWarp = 12;      // the first of kWidenWarps for K, as many for V follow
 constexpr int kWidenWarps = 4;
 constexpr int kThreads = 32 * (kWidenWarp + 2 * kWidenWarps);
@@ -82,9 +89,36 @@ struct Params {
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group, tpt;  // tpt = tokens per query tile
   int max_blocks_per_seq, block_size, log2_block, num_blocks;
   uint32_t group_magic;  // ceil(2^16 / G): r / G = r * group_magic >> 16 for r < 128
-  int ncb;  // query blocks (of kTiles x tpt tokens) of the longest sequence
+  int max_blocks;  // query blocks (of kTiles x tpt tokens) taken of a sequence at most
   float scale_log2;
   unsigned* err;
+};
+
+// A work item as the claiming warp announces it.
+struct Item {
+  int run;  // 0: no more items, 1: attend, 2: an impossible sequence, zeros
+  int g;    // kv head
+  int qs, qlen, ctx, tok0;  // the sequence's first row of q, rows, context; the item's first token
+  int s;
+  int bad;  // a block id of its keys is out of range
+};
+
+// Keys that query tile t of an item needs, in tiles: up to the position of its last token.
+__device__ __forceinline__ int key_tiles(const Item& it, int t, int tpt) {
+  const int ntok = min(tpt, it.qlen - (it.tok0 + t * tpt));
+  return it.run == 1 && ntok > 0 ? (it.ctx - it.qlen + it.tok0 + t * tpt + ntok - 1) / kKeys + 1 : 0;
+}
+
+// A place in a ring of kStages and the parity of its current use.
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == kStages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
 };
 
 template <int D>
@@ -96,22 +130,43 @@ struct Smem {
   // scales over their reference
   uint8_t raw[2][2][kKeys * D];
   float ratio[2][2][kGroups];
-  float kref[16], vref[16];            // of key tile kt at kt % 16
-  unsigned long long q_full, q_ready;  // Q has landed; bf16 rows are f16 rows
+  float kref[16], vref[16];            // of key tile number T (over all items) at T % 16
+  uint8_t stage[8][32 * 128];          // per softmax warp: 64 columns of its rows on their way out
+  uint4 claim;                         // the answer to a claim
+  Item item[kItems];
+  unsigned long long item_full[kItems], item_free[kItems], claim_full;
+  float q_factor[kTiles][kRows];       // bf16 rows of q: what turns their f16 products back
+  unsigned long long q_full, q_ready, q_free[kTiles];  // rows landed / are f16 / last S done
   unsigned long long raw_full[2][2], raw_free[2][2];
   unsigned long long k_full[kStages], v_full[kStages];
   unsigned long long s_full[kTiles][2], p_full[kTiles][2];
-  unsigned long long o_done[kTiles][kStages];  // P V of tile kt done (frees stage kt % kStages)
-  unsigned long long fin;  // the MMA warps' last commits
+  unsigned long long o_done[kTiles][kStages];  // P V of the key tile in that stage done (frees it)
+  // P V number i of the query tile done, at i % 2: the last two may both be under way when the
+  // softmax waits, and a wait tells only neighbouring phases of a barrier apart
+  unsigned long long pv_done[kTiles][2];
+  unsigned long long fin[kTiles];              // an MMA warp's last commit
   uint32_t tmem;
-  int bad;    // a block id of this CTA's keys is out of range
   int abort;  // a wait gave up: every role stops
 };
 
 #define PA_R4(a) "=r"(r[a]), "=r"(r[a + 1]), "=r"(r[a + 2]), "=r"(r[a + 3])
 #define PA_R16(a) PA_R4(a), PA_R4(a + 4), PA_R4(a + 8), PA_R4(a + 12)
-// 64 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+// 32 or 64 consecutive fp32 columns of this thread's TMEM lane.  The load and its wait are one
+// statement: arithmetic on the loaded registers cannot be scheduled between the two.
+__device__ __forceinline__ void tmem_get32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : PA_R16(0), PA_R16(16)
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_get64(uint32_t taddr, float (&v)[64]) {
   uint32_t r[64];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
@@ -164,6 +219,28 @@ __device__ __forceinline__ uint32_t elect_one() {
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(el));
   return el;
+}
+
+// Ask for the work of a CTA of this grid that has not started; the answer (16 bytes) lands at
+// `to`, counted on `bar`.
+__device__ __forceinline__ void claim_ask(uint32_t to, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+      "r"(bar)
+      : "memory");
+}
+// The claimed CTA's x index, or -1 when none was left.
+__device__ __forceinline__ int claim_answer(uint32_t from) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(from)
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
 }
 
 // Eight codes (two words) times a ratio -> eight f16 values.
@@ -249,47 +326,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform over the warp)
-  // Launch order: the later half of every sequence's query blocks (the most keys) first, then
-  // the earlier half, latest block first within each, so that the long CTAs do not come last;
-  // the blocks of one (sequence, kv head) stay together and share their K/V in L2.
-  const int s = blockIdx.y, g = blockIdx.z % p.num_kv_heads, half = blockIdx.z / p.num_kv_heads;
-  const int nearly = p.ncb - static_cast<int>(gridDim.x);  // blocks in the earlier half
-  if (half == 1 && static_cast<int>(blockIdx.x) >= nearly) return;  // (uniform over the CTA)
-  const int cb = (half == 0 ? p.ncb : nearly) - 1 - static_cast<int>(blockIdx.x);
-  const int qs = __ldg(p.query_start + s), qe = __ldg(p.query_start + s + 1);
-  if (qs < 0 || qe < qs || qe > p.num_tokens) {  // rows that are not q's: nothing is touched
-    if (tid == 0) atomicOr(p.err, kErrBadContext);
-    return;
-  }
-  const int qlen = qe - qs;
   const int tpt = p.tpt, G = p.group;
-  const int tok0 = cb * kTiles * tpt;
-  if (tok0 >= qlen) return;  // (uniform over the CTA)
-  const int ctx = __ldg(p.context_lens + s);
   T* outp = reinterpret_cast<T*>(p.out);
-  if (ctx < 1 || ctx > p.max_blocks_per_seq * p.block_size || qlen > ctx) {
-    const int ntok = min(kTiles * tpt, qlen - tok0);
-    for (int i = tid; i < ntok * G * CH; i += kThreads) {
-      const int r = i / CH, c = i % CH;
-      reinterpret_cast<uint4*>(outp + ((static_cast<size_t>(qs + tok0 + r / G) * p.num_q_heads +
-                                        g * G + r % G) * D))[c] = make_uint4(0, 0, 0, 0);
-    }
-    if (tid == 0) atomicOr(p.err, kErrBadContext);
-    return;
-  }
-  // key tiles each query tile needs: up to the position of its last token
-  int nt[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int ntok = min(tpt, qlen - (tok0 + t * tpt));
-    nt[t] = ntok > 0 ? (ctx - qlen + tok0 + t * tpt + ntok - 1) / kKeys + 1 : 0;
-  }
-  const int n = max(nt[0], nt[1]);
 
-  // ---- set-up: barriers, the first query rows on their way, tensor memory ----
+  // ---- set-up: barriers, tensor memory ----
   if (warp == kMmaWarp && lane == 0) {
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(smem_addr(&sm.item_full[i]), 1);
+      // every warp but the claiming one
+      mbar_init(smem_addr(&sm.item_free[i]), kThreads / 32 - 1);
+    }
+    mbar_init(smem_addr(&sm.claim_full), 1);
     mbar_init(smem_addr(&sm.q_full), 33);  // TMA expect-tx + 32 copy lanes
-    mbar_init(smem_addr(&sm.q_ready), kTiles * kRows);
+    mbar_init(smem_addr(&sm.q_ready), 2 * kWidenWarps);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_addr(&sm.raw_full[i >> 1][i & 1]), 1);
       mbar_init(smem_addr(&sm.raw_free[i >> 1][i & 1]), kWidenWarps);
@@ -300,30 +349,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       for (int t = 0; t < kTiles; ++t) mbar_init(smem_addr(&sm.o_done[t][i]), 1);
     }
     for (int t = 0; t < kTiles; ++t) {
+      mbar_init(smem_addr(&sm.q_free[t]), 1);
+      mbar_init(smem_addr(&sm.fin[t]), 1);
       for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&sm.pv_done[t][b]), 1);
         mbar_init(smem_addr(&sm.s_full[t][b]), 2);  // the MMA warp, its MMAs
         mbar_init(smem_addr(&sm.p_full[t][b]), kRows / 32);
       }
     }
-    mbar_init(smem_addr(&sm.fin), kTiles);
     fence_mbar_init();
-    sm.bad = 0;
     sm.abort = 0;
-    // A whole query tile (tpt tokens x G heads = 128 rows, each token's G rows contiguous in
-    // q) comes by TMA, one copy per 64-column half.
-    uint32_t tma_bytes = 0;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-      if (p.q_tma && tok0 + (t + 1) * tpt <= qlen) tma_bytes += kRows * D * 2;
-    mbar_arrive_expect_tx(smem_addr(&sm.q_full), tma_bytes);
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      if (!(p.q_tma && tok0 + (t + 1) * tpt <= qlen)) continue;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, g * G, qs + tok0 + t * tpt,
-                    smem_addr(&sm.q_full));
-    }
   }
   if (warp == kMmaWarp + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -340,6 +375,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
     if (mbar_wait_bounded(smem_addr(&bar), static_cast<uint32_t>(parity), &sm.abort)) return true;
     if (atomicExch(&sm.abort, 1) == 0) atomicOr(p.err, kErrTimeout);
     return false;
+  };
+
+  auto wwait = [&](unsigned long long& bar, uint32_t parity) -> bool {  // warp-uniform result
+    return __all_sync(0xffffffffu, wait(bar, static_cast<int>(parity))) != 0;
+  };
+  // Item number j, once it is announced (false: a wait gave up).  A role hands it back with
+  // item_done when it has no more use for the slot.
+  auto item_get = [&](int j, Item& it) -> bool {
+    if (!wwait(sm.item_full[j % kItems], (j / kItems) & 1)) return false;
+    it = sm.item[j % kItems];
+    return true;
+  };
+  auto item_done = [&](int j) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sm.item_free[j % kItems]));
   };
 
   if (warp >= kMmaWarp) {
@@ -362,136 +412,284 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       const uint32_t ring = smem_addr(is_v ? sm.v[0] : sm.k[0]) + cw * 16 * 128;
       const uint32_t raw = smem_addr(sm.raw[is_v][0]) + cw * 16 * D + get;
       unsigned long long* full = is_v ? sm.v_full : sm.k_full;
-      for (int kt = 0; kt < n; ++kt) {
-        const int st = kt % kStages, b = kt & 1;
-        if (!wait(sm.raw_full[is_v][b], (kt >> 1) & 1)) break;
-        const float2 r = *reinterpret_cast<const float2*>(&sm.ratio[is_v][b][2 * cw]);
-        uint4 c[2][NH];
-#pragma unroll
-        for (int gi = 0; gi < 2; ++gi)
-#pragma unroll
-          for (int hc = 0; hc < NH; ++hc)
-            c[gi][hc] = ld_shared16((raw ^ (hc * 64)) + b * (kKeys * D) + gi * 8 * D);
-        // (the row of group gi: kt * 64 + 16 cw + 8 gi + rr)
-        const int left = ctx - (kt * kKeys + 16 * cw + rr);
-        if (left <= 8) {
+      Ring r3;
+      uint32_t num = 0, loads = 0;  // key tiles and q loads so far
+      Item it;
+      bool ok = true;
+      for (int j = 0; ok && (ok = item_get(j, it)) && it.run; ++j) {
+        item_done(j);
+        const int n = max(key_tiles(it, 0, tpt), key_tiles(it, 1, tpt));
+        // bf16 rows of q become f16 rows here, a row per lane: V's warps take query tile 0 before
+        // their first tile, K's take query tile 1 after theirs.  (The softmax warps, busy writing
+        // the last item out, took 7000 cycles from its last P V to the next item's first S.)
+        auto q_rows = [&](int t) -> bool {
+          if (!wwait(sm.q_full, loads & 1)) return false;
+          ++loads;
+          if (key_tiles(it, t, tpt) > 0)
+            sm.q_factor[t][32 * cw + lane] = q_row_to_f16<D>(smem_addr(sm.q[t]), 32 * cw + lane);
+          fence_async_smem();  // the rows before the tensor cores' reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.q_ready));
+          return true;
+        };
+        if (BF && is_v && n > 0 && !(ok = q_rows(0))) break;
+        for (int kt = 0; kt < n; ++kt, ++num, r3.next()) {
+          const int b = num & 1;
+          if (!(ok = wwait(sm.raw_full[is_v][b], (num >> 1) & 1))) break;
+          const float2 r = *reinterpret_cast<const float2*>(&sm.ratio[is_v][b][2 * cw]);
+          uint4 c[2][NH];
 #pragma unroll
           for (int gi = 0; gi < 2; ++gi)
-            if (left <= 8 * gi) {
 #pragma unroll
-              for (int hc = 0; hc < NH; ++hc) c[gi][hc] = make_uint4(0, 0, 0, 0);
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.raw_free[is_v][b]));
-        if (kt >= kStages && !(wait(sm.o_done[0][st], (kt / kStages - 1) & 1) &&
-                               wait(sm.o_done[1][st], (kt / kStages - 1) & 1)))
-          break;
-        const uint32_t tile = ring + st * (kKeys * D * 2);
+            for (int hc = 0; hc < NH; ++hc)
+              c[gi][hc] = ld_shared16((raw ^ (hc * 64)) + b * (kKeys * D) + gi * 8 * D);
+          // (the row of group gi: kt * 64 + 16 cw + 8 gi + rr)
+          const int left = it.ctx - (kt * kKeys + 16 * cw + rr);
+          if (left <= 8) {
 #pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-          const __half2 ratio = __float2half2_rn(gi ? r.y : r.x);
+            for (int gi = 0; gi < 2; ++gi)
+              if (left <= 8 * gi) {
 #pragma unroll
-          for (int hc = 0; hc < NH; ++hc) {
-            const uint32_t at = tile + 8 * gi * 128 + hc * (kKeys * 128);
-            st_shared16(at + put0, widen8(c[gi][hc].x, c[gi][hc].y, ratio));
-            st_shared16(at + put1, widen8(c[gi][hc].z, c[gi][hc].w, ratio));
+                for (int hc = 0; hc < NH; ++hc) c[gi][hc] = make_uint4(0, 0, 0, 0);
+              }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.raw_free[is_v][b]));
+          if (num >= kStages &&
+              !(ok = wwait(sm.o_done[0][r3.st], r3.ph ^ 1u) && wwait(sm.o_done[1][r3.st], r3.ph ^ 1u)))
+            break;
+          const uint32_t tile = ring + r3.st * (kKeys * D * 2);
+#pragma unroll
+          for (int gi = 0; gi < 2; ++gi) {
+            const __half2 ratio = __float2half2_rn(gi ? r.y : r.x);
+#pragma unroll
+            for (int hc = 0; hc < NH; ++hc) {
+              const uint32_t at = tile + 8 * gi * 128 + hc * (kKeys * 128);
+              st_shared16(at + put0, widen8(c[gi][hc].x, c[gi][hc].y, ratio));
+              st_shared16(at + put1, widen8(c[gi][hc].z, c[gi][hc].w, ratio));
+            }
+          }
+          fence_async_smem();  // these stores before the tensor cores' reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&full[r3.st]));
+          if (BF && !is_v && kt == 0 && !(ok = q_rows(1))) break;
         }
-        fence_async_smem();  // these stores before the tensor cores' reads
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&full[st]));
       }
     } else if (warp >= kCodeWarp) {
-      // ===== blocks, scales and codes of K (or V): a tile ahead of the widening warps =====
-      // Lane g < 8 looks after token group g of a tile.
+      // ===== items, blocks, scales and codes of K (or V), ahead of the widening warps =====
       const int is_v = warp != kCodeWarp;
-      const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-      // does tile kt's group hold keys that are used
-      auto used = [&](int kt) -> bool { return lane < kGroups && kt < n && kt * kKeys + 8 * lane < ctx; };
-      // its table entry; checked a tile later, when it is used, so that nothing waits for the
-      // load (the loads here are volatile to stay where they are written)
-      auto entry = [&](int kt) -> int {
-        return used(kt) ? static_cast<int>(ld_early(trow + ((kt * kKeys + 8 * lane) >> p.log2_block))) : -1;
-      };
-      auto block_of = [&](int kt, int e) -> int {
-        if (e >= 0 && e < p.num_blocks) return e;
-        if (used(kt)) sm.bad = 1;
-        return -1;
-      };
-      auto scale_of = [&](const float* scales, int e) -> float {
-        return e >= 0 ? __uint_as_float(ld_early(scales + static_cast<size_t>(e) * p.num_kv_heads + g)) : 0.f;
-      };
-      const int raw0 = entry(0);
-      int raw_e = entry(1);
-      int e = block_of(0, raw0);
-      // (K's warp follows the V scales too: it tells the softmax both references)
-      float sk = is_v ? 0.f : scale_of(p.k_scales, e), sv = scale_of(p.v_scales, e);
-      float vref = 0.f;
-      const bool first_group = ((8 * lane) & (p.block_size - 1)) == 0;  // of its block
-      for (int kt = 0; kt < n; ++kt) {
-        const int e1 = block_of(kt + 1, raw_e);
-        const float sk1 = is_v ? 0.f : scale_of(p.k_scales, e1), sv1 = scale_of(p.v_scales, e1);
-        raw_e = entry(kt + 2);
-        // (scales are positive, so their bits order as integers)
-        const float kref = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sk)));
-        const float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv)));
-        if (kt == 0 || vtop > vref * kScaleRoom) vref = vtop;
-        const float ref = is_v ? vref : kref;
-        const float ratio = ref > 0.f ? (is_v ? sv : sk) * __frcp_rn(ref) : 0.f;
-        const int b = kt & 1;
-        if (kt >= 2 && !wait(sm.raw_free[is_v][b], (kt / 2 - 1) & 1)) break;
-        // free: tile kt - 2 is read, with its ratios; K's tile kt - 3 is widened, so the P V of
-        // kt - 7 is done, and the softmax of kt - 16 is long done with its references
-        if (lane < kGroups) sm.ratio[is_v][b][lane] = ratio;
-        if (lane == 0 && !is_v) {
-          sm.kref[kt & 15] = kref;
-          sm.vref[kt & 15] = vref;
+      const int per_item = kTiles * tpt;
+      // K's warp claims the items.  Item x of the grid: kv head x % Hkv of query block x / Hkv,
+      // the blocks of all sequences counted from the last one's last block down, so that a
+      // sequence's long items come first; items past the last block (the grid is sized without
+      // knowing the lengths) end the CTA.  Lane u keeps the blocks of sequences [u * per,
+      // (u + 1) * per): `mine` of them, `before` of lower lanes.
+      const int per = (p.num_seqs + 31) / 32;
+      auto blocks_of = [&](int s) -> int {
+        if (s >= p.num_seqs) return 0;
+        const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
+        if (a < 0 || b < a || b > p.num_tokens) {  // rows that are not q's: nothing is touched
+          atomicOr(p.err, kErrBadContext);
+          return 0;
         }
-        const bool mine = first_group && e >= 0;  // (e < 0 past the groups)
-        const uint32_t blocks = __ballot_sync(0xffffffffu, mine);
-        __syncwarp();  // the stores above before the arrival
-        if (lane == 0)
-          mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]),
-                                static_cast<uint32_t>(__popc(blocks) * p.block_size * D));
-        __syncwarp();
-        if (mine)
-          tma_load_4d(smem_addr(sm.raw[is_v][b]) + 8 * lane * D, is_v ? &p.vmap : &p.kmap, 0, 0, g, e,
-                      smem_addr(&sm.raw_full[is_v][b]));
-        e = e1;
-        sk = sk1;
-        sv = sv1;
-      }
-    } else {
-      if (warp == kMmaWarp) {
-        // ===== query tiles that run past their sequence (the whole ones are on their way) =====
-        // by 16-byte copies; rows past the last token are zeros
+        return min(p.max_blocks, (b - a + per_item - 1) / per_item);
+      };
+      auto scan32 = [&](int x) -> int {  // inclusive sum over the lanes
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const int first = tok0 + t * tpt;
-          if (first >= qlen || (p.q_tma && first + tpt <= qlen)) continue;
-          // (rows past tpt * G, where G does not divide 128, are zeros too)
-          for (int u = lane; u < kRows * CH; u += 32) {
-            const int r = u / CH, c = u % CH;
-            const int tok = first + r / G;
-            const bool live = r < tpt * G && tok < qlen;
-            const uint8_t* src = p.q + ((static_cast<size_t>(qs + (live ? tok : 0)) * p.num_q_heads +
-                                         g * G + (live ? r % G : 0)) * D + c * 8) * 2;
-            cp_async16(smem_addr(sm.q[t]) + swz(kRows, r, c), src, live ? 16u : 0u);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        return x;
+      };
+      int mine = 0, before = 0, total = 0;
+      if (!is_v) {
+        for (int i = 0; i < per; ++i) mine += blocks_of(lane * per + i);
+        const int incl = scan32(mine);
+        before = incl - mine;
+        total = __shfl_sync(0xffffffffu, incl, 31);
+      }
+      auto item_of = [&](int x) -> Item {  // (uniform over the warp)
+        Item it;
+        it.run = it.bad = 0;
+        const int f = total - 1 - x / p.num_kv_heads;  // query block, counted from the first
+        it.g = x % p.num_kv_heads;
+        if (x < 0 || f < 0) return it;
+        const int owner = 31 - __clz(__ballot_sync(0xffffffffu, before <= f && mine > 0));
+        int left = f - __shfl_sync(0xffffffffu, before, owner);
+        for (int s0 = owner * per; s0 < (owner + 1) * per; s0 += 32) {
+          const int nb = s0 + lane < (owner + 1) * per ? blocks_of(s0 + lane) : 0;
+          const int incl = scan32(nb);
+          const int sum = __shfl_sync(0xffffffffu, incl, 31);
+          if (left < sum) {
+            const int o = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
+            it.s = s0 + o;
+            left -= __shfl_sync(0xffffffffu, incl - nb, o);
+            it.run = 1;
+            break;
+          }
+          left -= sum;
+        }
+        if (!it.run) return it;  // (never: the block is one of the owner's)
+        it.qs = __ldg(p.query_start + it.s);
+        it.qlen = __ldg(p.query_start + it.s + 1) - it.qs;
+        it.ctx = __ldg(p.context_lens + it.s);
+        it.tok0 = left * per_item;
+        if (it.ctx < 1 || it.ctx > p.max_blocks_per_seq * p.block_size || it.qlen > it.ctx) {
+          it.run = 2;
+          if (lane == 0) atomicOr(p.err, kErrBadContext);
+        }
+        return it;
+      };
+      const bool first_group = ((8 * lane) & (p.block_size - 1)) == 0;  // of its block
+      uint32_t num = 0, claims = 0, loads = 0;  // key tiles, claims and q loads so far
+      Item it;
+      if (!is_v) it = item_of(blockIdx.x);
+      bool ok = true;
+      for (int j = 0; ok; ++j) {
+        if (is_v) {
+          if (!(ok = item_get(j, it))) break;
+        } else {
+          if (j >= kItems && !(ok = wwait(sm.item_free[j % kItems], (j / kItems - 1) & 1))) break;
+          if (lane == 0) {
+            sm.item[j % kItems] = it;
+            mbar_arrive(smem_addr(&sm.item_full[j % kItems]));
+          }
+          __syncwarp();
+        }
+        if (!it.run) break;
+        const int n = max(key_tiles(it, 0, tpt), key_tiles(it, 1, tpt));
+        if (is_v) {
+          item_done(j);
+          if (it.run == 1) {
+            // ===== q: once the last item's S are done =====
+            // A whole query tile (tpt tokens x G heads = 128 rows, each token's G rows
+            // contiguous in q) by TMA, one copy per 64-column half; a tile that runs past its
+            // sequence by 16-byte copies, rows past the last token zeros.
+            if (loads > 0 && !(ok = wwait(sm.q_free[0], (loads - 1) & 1) && wwait(sm.q_free[1], (loads - 1) & 1)))
+              break;
+            ++loads;
+            if (lane == 0) {
+              uint32_t tma_bytes = 0;
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t)
+                if (p.q_tma && it.tok0 + (t + 1) * tpt <= it.qlen) tma_bytes += kRows * D * 2;
+              mbar_arrive_expect_tx(smem_addr(&sm.q_full), tma_bytes);
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                if (!(p.q_tma && it.tok0 + (t + 1) * tpt <= it.qlen)) continue;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, it.g * G,
+                              it.qs + it.tok0 + t * tpt, smem_addr(&sm.q_full));
+              }
+            }
+            __syncwarp();
+            for (int t = 0; t < kTiles; ++t) {
+              const int first = it.tok0 + t * tpt;
+              if (first >= it.qlen || (p.q_tma && first + tpt <= it.qlen)) continue;
+              // (rows past tpt * G, where G does not divide 128, are zeros too)
+              for (int u = lane; u < kRows * CH; u += 32) {
+                const int r = u / CH, c = u % CH;
+                const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
+                const bool live = tl < tpt && first + tl < it.qlen;
+                const uint8_t* src =
+                    p.q + ((static_cast<size_t>(it.qs + (live ? first + tl : 0)) * p.num_q_heads +
+                            it.g * G + (live ? r - tl * G : 0)) * D + c * 8) * 2;
+                cp_async16(smem_addr(sm.q[t]) + swz(kRows, r, c), src, live ? 16u : 0u);
+              }
+            }
+            cp_async_arrive(smem_addr(&sm.q_full));
           }
         }
-        cp_async_arrive(smem_addr(&sm.q_full));
+        // Lane g < 8 looks after token group g of a tile.
+        const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
+        // does tile kt's group hold keys that are used
+        auto used = [&](int kt) -> bool { return lane < kGroups && kt < n && kt * kKeys + 8 * lane < it.ctx; };
+        // its table entry; checked a tile later, when it is used, so that nothing waits for the
+        // load (the loads here are volatile to stay where they are written)
+        auto entry = [&](int kt) -> int {
+          return used(kt) ? static_cast<int>(ld_early(trow + ((kt * kKeys + 8 * lane) >> p.log2_block))) : -1;
+        };
+        auto block_of = [&](int kt, int e) -> int {
+          if (e >= 0 && e < p.num_blocks) return e;
+          if (used(kt) && !is_v) {
+            sm.item[j % kItems].bad = 1;  // (read by the softmax when the item's tiles are done)
+            atomicOr(p.err, kErrBadBlock);
+          }
+          return -1;
+        };
+        auto scale_of = [&](const float* scales, int e) -> float {
+          return e >= 0 ? __uint_as_float(ld_early(scales + static_cast<size_t>(e) * p.num_kv_heads + it.g)) : 0.f;
+        };
+        const int raw0 = entry(0);
+        int raw_e = entry(1);
+        int e = block_of(0, raw0);
+        // (K's warp follows the V scales too: it tells the softmax both references)
+        float sk = is_v ? 0.f : scale_of(p.k_scales, e), sv = scale_of(p.v_scales, e);
+        float vref = 0.f;
+        for (int kt = 0; kt < n; ++kt, ++num) {
+          // the next item is claimed three tiles before this one's end: late, so that no SM
+          // sits on work that another could start, yet early enough for the answer
+          if (!is_v && kt == max(0, n - 3) && lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
+            claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
+          }
+          const int e1 = block_of(kt + 1, raw_e);
+          const float sk1 = is_v ? 0.f : scale_of(p.k_scales, e1), sv1 = scale_of(p.v_scales, e1);
+          raw_e = entry(kt + 2);
+          // (scales are positive, so their bits order as integers)
+          const float kref = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sk)));
+          const float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv)));
+          if (kt == 0 || vtop > vref * kScaleRoom) vref = vtop;
+          const float ref = is_v ? vref : kref;
+          const float ratio = ref > 0.f ? (is_v ? sv : sk) * __frcp_rn(ref) : 0.f;
+          const int b = num & 1;
+          if (num >= 2 && !(ok = wwait(sm.raw_free[is_v][b], ((num >> 1) - 1) & 1))) break;
+          // free: the tile two back is read, with its ratios; K's tile three back is widened, so
+          // the P V of six back is done, and the softmax of 16 back is long done with its
+          // references
+          if (lane < kGroups) sm.ratio[is_v][b][lane] = ratio;
+          if (lane == 0 && !is_v) {
+            sm.kref[num & 15] = kref;
+            sm.vref[num & 15] = vref;
+          }
+          const bool mine_now = first_group && e >= 0;  // (e < 0 past the groups)
+          const uint32_t blocks = __ballot_sync(0xffffffffu, mine_now);
+          __syncwarp();  // the stores above before the arrival
+          if (lane == 0)
+            mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]),
+                                  static_cast<uint32_t>(__popc(blocks) * p.block_size * D));
+          __syncwarp();
+          if (mine_now)
+            tma_load_4d(smem_addr(sm.raw[is_v][b]) + 8 * lane * D, is_v ? &p.vmap : &p.kmap, 0, 0, it.g, e,
+                        smem_addr(&sm.raw_full[is_v][b]));
+          e = e1;
+          sk = sk1;
+          sv = sv1;
+        }
+        if (!ok) break;
+        if (!is_v) {
+          if (n == 0 && lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
+            claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
+          }
+          if (!(ok = wwait(sm.claim_full, claims & 1))) break;
+          ++claims;
+          const int x = claim_answer(smem_addr(&sm.claim));
+          fence_async_smem();  // the read above before the next answer
+          __syncwarp();
+          it = item_of(x);
+        }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
       // ============ MMA issue: a warp per query tile ============
-      // The tensor pipe runs one thread's MMAs in order, so S of key tile kt + 1 may overwrite
-      // the P of kt - 1, whose P V was issued before it.  A warp whose query tile needs no more
-      // keys still frees each stage, after it has landed.
+      // The tensor pipe runs one thread's MMAs in order, so S of a key tile may overwrite the P
+      // of the tile two before, whose P V was issued earlier.  A warp whose query tile needs no
+      // more keys still frees each stage, after it has landed.
       const int t = warp - kMmaWarp;
-      const int ntt = t == 0 ? nt[0] : nt[1];
       const uint32_t el = elect_one();
-      auto wwait = [&](unsigned long long& bar, int parity) -> bool {  // warp-uniform result
-        return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
-      };
       constexpr uint32_t id_s = idesc_f16<__half>(kRows, kKeys, false);
       constexpr uint32_t id_o = idesc_f16<__half>(kRows, D, true);
       constexpr uint32_t kStageBytes = kKeys * D * 2;
@@ -499,198 +697,221 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       const uint64_t dk0 = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
       const uint64_t dv0 = desc_sw128(smem_addr(sm.v[0]), kKeys * 128, 1024);
       const uint32_t cols = tmem + t * kTileCols;
-      auto issue_s = [&](int kt) {
-        const uint32_t d = cols + (kt & 1) * kColS;
-        const uint64_t kd = dk0 + (((kt % kStages) * kStageBytes) >> 4);
+      auto issue_s = [&](uint32_t sn, int st) {  // S number sn of this query tile, K in stage st
+        const uint32_t d = cols + (sn & 1) * kColS;
+        const uint64_t kd = dk0 + ((st * kStageBytes) >> 4);
 #pragma unroll
         for (int ks = 0; ks < KS1; ++ks)  // 16 columns = 32 bytes of 64-column block ks / 4
           mma_el(d, qd + (((ks >> 2) * kRows * 128 + (ks & 3) * 32) >> 4),
                  kd + (((ks >> 2) * kKeys * 128 + (ks & 3) * 32) >> 4), id_s, ks > 0, el);
-        commit_el(smem_addr(&sm.s_full[t][kt & 1]), el);
-        if (el) mbar_arrive(smem_addr(&sm.s_full[t][kt & 1]));  // (passes k_full on to the softmax)
+        commit_el(smem_addr(&sm.s_full[t][sn & 1]), el);
+        if (el) mbar_arrive(smem_addr(&sm.s_full[t][sn & 1]));  // (passes k_full on to the softmax)
       };
-      auto issue_pv = [&](int kt) {
-        const uint32_t pa = cols + (kt & 1) * kColS, o = cols + kColO;
-        const uint64_t vd = dv0 + (((kt % kStages) * kStageBytes) >> 4);
+      auto issue_pv = [&](uint32_t sn, int st, bool first) {
+        const uint32_t pa = cols + (sn & 1) * kColS, o = cols + kColO;
+        const uint64_t vd = dv0 + ((st * kStageBytes) >> 4);
 #pragma unroll
         for (int ks = 0; ks < KS2; ++ks)  // 16 keys = 8 columns of P
-          mma_ts_el(o, pa + ks * 8, vd + ((ks * 16 * 128) >> 4), id_o, kt > 0 || ks > 0, el);
+          mma_ts_el(o, pa + ks * 8, vd + ((ks * 16 * 128) >> 4), id_o, !first || ks > 0, el);
       };
-      bool ok = wwait(BF ? sm.q_ready : sm.q_full, 0);
-      fence_async_smem();  // q rows that lanes copied or converted -> tensor cores
-      ok = ok && wwait(sm.k_full[0], 0);
-      if (ok && ntt > 0) issue_s(0);
-      for (int kt = 0; ok && kt < n; ++kt) {
-        const int st = kt % kStages;
-        if (kt + 1 < ntt) {
-          if (!(ok = wwait(sm.k_full[(kt + 1) % kStages], ((kt + 1) / kStages) & 1))) break;
-          issue_s(kt + 1);
+      Ring rk, rv;
+      uint32_t sn = 0, loads = 0;  // S issued for this query tile, q loads so far
+      Item it;
+      bool ok = true;
+      for (int j = 0; ok && (ok = item_get(j, it)); ++j) {
+        if (!__shfl_sync(0xffffffffu, it.run, 0)) break;
+        item_done(j);
+        // (broadcast, so that the loops are known to be uniform)
+        const int n0 = key_tiles(it, 0, tpt), n1 = key_tiles(it, 1, tpt);
+        const int n = __shfl_sync(0xffffffffu, max(n0, n1), 0);
+        const int ntt = __shfl_sync(0xffffffffu, t == 0 ? n0 : n1, 0);
+        if (n == 0) continue;
+        if (!(ok = wwait(BF ? sm.q_ready : sm.q_full, loads & 1))) break;
+        ++loads;
+        fence_async_smem();  // q rows that lanes copied or converted -> tensor cores
+        if (ntt > 0) {
+          if (!(ok = wwait(sm.k_full[rk.st], rk.ph))) break;
+          issue_s(sn, rk.st);
         }
-        if (!(ok = wwait(sm.v_full[st], (kt / kStages) & 1))) break;
-        if (kt < ntt) {
-          if (!(ok = wwait(sm.p_full[t][kt & 1], (kt >> 1) & 1))) break;
-          tc_fence_after();
-          issue_pv(kt);
-        } else if (!(ok = wwait(sm.k_full[st], (kt / kStages) & 1))) {
-          break;
+        rk.next();
+        if (ntt <= 1) commit_el(smem_addr(&sm.q_free[t]), el);
+        for (int kt = 0; kt < n; ++kt, rk.next(), rv.next()) {
+          if (kt + 1 < ntt) {
+            if (!(ok = wwait(sm.k_full[rk.st], rk.ph))) break;
+            issue_s(sn + 1, rk.st);
+            if (kt + 2 == ntt) commit_el(smem_addr(&sm.q_free[t]), el);
+          }
+          if (!(ok = wwait(sm.v_full[rv.st], rv.ph))) break;
+          if (kt < ntt) {
+            if (!(ok = wwait(sm.p_full[t][sn & 1], (sn >> 1) & 1))) break;
+            tc_fence_after();
+            issue_pv(sn, rv.st, kt == 0);
+            commit_el(smem_addr(&sm.pv_done[t][sn & 1]), el);
+            ++sn;
+          } else if (!(ok = wwait(sm.k_full[rv.st], rv.ph))) {
+            break;
+          }
+          commit_el(smem_addr(&sm.o_done[t][rv.st]), el);
         }
-        commit_el(smem_addr(&sm.o_done[t][st]), el);
+        // rk ran one tile ahead of rv, past the item's end
+        rk = rv;
       }
-      commit_el(smem_addr(&sm.fin), el);  // every MMA this warp issued
-      wwait(sm.fin, 0);
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      commit_el(smem_addr(&sm.fin[t]), el);  // every MMA this warp issued
+      wwait(sm.fin[t], 0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ================= softmax: warpgroup t, one thread per row =================
     const int t = warp >> 2, r = tid & (kRows - 1);
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + t * kTileCols;
-    const int tok = tok0 + t * tpt + r / G;
-    const bool row_ok = r / G < tpt && tok < qlen;
-    const int pos = row_ok ? ctx - qlen + tok : -1;
-    const int pos_lo = ctx - qlen + tok0 + t * tpt;  // the tile's first position
-    float m_used = -INFINITY, l_run = 0.f, vref = 0.f;
+    const int tile_tok = static_cast<int>((r * p.group_magic) >> 16);  // r / G
+    uint32_t sn = 0, num = 0;  // S of this query tile and key tiles so far
+    Item it;
     bool ok = true;
-    auto wwait = [&](unsigned long long& bar, int parity) -> bool {  // warp-uniform result
-      return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
-    };
-    float row_scale = p.scale_log2;  // of this row's scores, before the key tile's kref
-    if constexpr (BF) {
-      ok = wwait(sm.q_full, 0);
-      if (ok && nt[t] > 0) row_scale *= q_row_to_f16<D>(smem_addr(sm.q[t]), r);
-      fence_async_smem();  // the row before the tensor cores' reads
-      mbar_arrive(smem_addr(&sm.q_ready));
-    }
-    for (int kt = 0; ok && kt < nt[t]; ++kt) {
-      const int b = kt & 1;
-      // (kref and vref were written before k_full of this tile, which the MMA warp acquired
-      // before it arrived here)
-      if (!(ok = wwait(sm.s_full[t][b], (kt >> 1) & 1))) break;
-      tc_fence_after();
-      // the tile's factor of the raw scores, positive (so that the maximum commutes with it and
-      // a masked -inf stays -inf even where it would underflow)
-      const float c = fmaxf(sm.kref[kt & 15] * row_scale, 1e-37f);
-      const float vnew = sm.vref[kt & 15];
-      float sv[kKeys];
-      tmem_ld64(tl + b * kColS, sv);
-      if (kt * kKeys + kKeys - 1 > pos_lo) {  // causal mask: key kt * 64 + i > pos
-        const int lim = pos - kt * kKeys;
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i)
-          if (i > lim) sv[i] = -INFINITY;
-      }
-      float pm[4];  // four chains of three-input maxima
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pm[j] = fmaxf(sv[2 * j], sv[2 * j + 1]);
-#pragma unroll
-      for (int i = 8; i < kKeys; i += 8)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pm[j] = fmax3(pm[j], sv[i + 2 * j], sv[i + 2 * j + 1]);
-      const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-      const float m_new = fmaxf(m_used, mx * c);
-      const bool need = kt > 0 && m_new > m_used + kRescale;
-      const bool moved = kt > 0 && vnew != vref;  // (uniform over the CTA)
-      if (moved || __any_sync(0xffffffffu, need)) {
-        // rescale O, once P V of tile kt - 1 is done (that of kt - 2 was issued before this S)
-        if (!(ok = wwait(sm.o_done[t][(kt - 1) % kStages], ((kt - 1) / kStages) & 1))) break;
+    for (int j = 0; ok && (ok = item_get(j, it)) && it.run; ++j) {
+      const int n0 = key_tiles(it, 0, tpt), n1 = key_tiles(it, 1, tpt);
+      const int n = max(n0, n1), ntt = t == 0 ? n0 : n1;
+      const int tok = it.tok0 + t * tpt + tile_tok;
+      const int pos = tile_tok < tpt && tok < it.qlen ? it.ctx - it.qlen + tok : -1;
+      const int pos_lo = it.ctx - it.qlen + it.tok0 + t * tpt;  // the tile's first position
+      float m_used = -INFINITY, l_run = 0.f, vref = 0.f;
+      float row_scale = p.scale_log2;  // of this row's scores, before the key tile's kref
+      for (int kt = 0; kt < ntt; ++kt, ++sn) {
+        const int b = sn & 1;
+        // (kref and vref were written before k_full of this tile, q_factor before q_ready, which
+        // the MMA warp acquired before it arrived here)
+        if (!(ok = wwait(sm.s_full[t][b], (sn >> 1) & 1))) break;
         tc_fence_after();
-        float alpha = need ? ex2(m_used - m_new) : 1.f;
-        if (need) {
-          l_run *= alpha;
-          m_used = m_new;
+        if (BF && kt == 0) row_scale *= sm.q_factor[t][r];
+        // the tile's factor of the raw scores, positive (so that the maximum commutes with it
+        // and a masked -inf stays -inf even where it would underflow)
+        const float c = fmaxf(sm.kref[(num + kt) & 15] * row_scale, 1e-37f);
+        const float vnew = sm.vref[(num + kt) & 15];
+        float sv[kKeys];
+        tmem_get64(tl + b * kColS, sv);
+        if (kt * kKeys + kKeys - 1 > pos_lo) {  // causal mask: key kt * 64 + i > pos
+          const int lim = pos - kt * kKeys;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (i > lim) sv[i] = -INFINITY;
         }
-        if (moved) alpha *= vref / vnew;
+        float pm[4];  // four chains of three-input maxima
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          tmem_ld32(tl + kColO + c0, o);
+        for (int q = 0; q < 4; ++q) pm[q] = fmaxf(sv[2 * q], sv[2 * q + 1]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(tl + kColO + c0, o);
+        for (int i = 8; i < kKeys; i += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) pm[q] = fmax3(pm[q], sv[i + 2 * q], sv[i + 2 * q + 1]);
+        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        const float m_new = fmaxf(m_used, mx * c);
+        const bool need = kt > 0 && m_new > m_used + kRescale;
+        const bool moved = kt > 0 && vnew != vref;  // (uniform over the CTA)
+        if (moved || __any_sync(0xffffffffu, need)) {
+          // rescale O, once P V of the tile before is done (the one before that was issued
+          // before this S)
+          if (!(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
+          tc_fence_after();
+          float alpha = need ? ex2(m_used - m_new) : 1.f;
+          if (need) {
+            l_run *= alpha;
+            m_used = m_new;
+          }
+          if (moved) alpha *= vref / vnew;
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_get32(tl + kColO + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st32(tl + kColO + c0, o);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        if (kt == 0) m_used = m_new;
+        vref = vnew;
+        // P = 2^(s c - m), rounded to f16, packed two a column over the first half of this
+        // thread's own row of S (already in registers); a row with nothing unmasked yet has
+        // every score at -inf, so any finite offset gives it P = 0
+        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
+        float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 x = __ffma2_rn(make_float2(sv[32 * h + i], sv[32 * h + i + 1]), c2, nm2);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            ps[(i >> 1) & 3] = __fadd2_rn(ps[(i >> 1) & 3], e);
+            pk[i >> 1] = pack2<__half>(e.x, e.y);
+          }
+          tmem_st16(tl + b * kColS + 16 * h, pk);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();  // the P stores before the MMA warp reads them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[t][b]));
+        const float2 s01 = __fadd2_rn(ps[0], ps[1]), s23 = __fadd2_rn(ps[2], ps[3]);
+        const float2 sall = __fadd2_rn(s01, s23);
+        l_run += sall.x + sall.y;
       }
-      if (kt == 0) m_used = m_new;
-      vref = vnew;
-      // P = 2^(s c - m), rounded to f16, packed two a column over the first half of this
-      // thread's own row of S (already in registers); a row with nothing unmasked yet has
-      // every score at -inf, so any finite offset gives it P = 0
-      const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-      const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
-      float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                      make_float2(0.f, 0.f)};
+      if (!ok) break;
+      if (ntt > 0 && !(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
+      tc_fence_after();
+      num += n;
+      // ---- out = O vref / l (the item's tiles are done, so its bad-block flag is final) ----
+      const bool good = it.run == 1 && ntt > 0 && *reinterpret_cast<volatile int*>(&sm.item[j % kItems].bad) == 0;
+      item_done(j);
+      const float inv = vref / l_run;
+      // The rows go out through shared memory, 64 columns at a time, so that each store
+      // instruction of a warp writes whole 128-byte lines.  Row r's 16-byte chunk c sits at
+      // chunk c ^ (r % 8) of its 128-byte staging row: neither the writes nor the reads
+      // collide in a bank.  (clamped: a cached f16 value may have been rounded up past 65504)
+      const uint32_t stage = smem_addr(sm.stage[warp]);
+      const int ch = lane & 7;
+      const int toks = min(tpt, it.qlen - (it.tok0 + t * tpt));  // tokens of this query tile
+      T* to = outp + (static_cast<size_t>(it.qs + it.tok0 + t * tpt) * p.num_q_heads + it.g * G) * D + ch * 8;
+      int at[8];  // of the eight rows that this lane stores a chunk of; -1: not a row
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16];
+      for (int i = 0; i < 8; ++i) {
+        const int row = (r - lane) + 4 * i + (lane >> 3);  // token tk of the tile, head row % G
+        const int tk = static_cast<int>((row * p.group_magic) >> 16);
+        at[i] = tk < toks ? (tk * (p.num_q_heads - G) + row) * D : -1;
+      }
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 x = __ffma2_rn(make_float2(sv[32 * h + i], sv[32 * h + i + 1]), c2, nm2);
-          const float2 e = make_float2(ex2(x.x), ex2(x.y));
-          ps[(i >> 1) & 3] = __fadd2_rn(ps[(i >> 1) & 3], e);
-          pk[i >> 1] = pack2<__half>(e.x, e.y);
+      for (int c0 = 0; c0 < D; c0 += 64) {
+#pragma unroll
+        for (int c1 = 0; c1 < 64; c1 += 32) {
+          float o[32];
+          if (good) tmem_get32(tl + kColO + c0 + c1, o);  // (uniform over the warp)
+          auto two = [&](int i) -> uint32_t {
+            const float2 x = __fmul2_rn(make_float2(o[i], o[i + 1]), inv2);
+            return good ? pack2_sat<T>(x.x, x.y) : 0u;
+          };
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+            st_shared16(stage + lane * 128 + (((c1 / 8 + cc) ^ (lane & 7)) << 4),
+                        make_uint4(two(8 * cc), two(8 * cc + 2), two(8 * cc + 4), two(8 * cc + 6)));
         }
-        tmem_st16(tl + b * kColS + 16 * h, pk);
-      }
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      tc_fence_before();  // the P stores before the MMA warp reads them
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[t][b]));
-      const float2 s01 = __fadd2_rn(ps[0], ps[1]), s23 = __fadd2_rn(ps[2], ps[3]);
-      const float2 sall = __fadd2_rn(s01, s23);
-      l_run += sall.x + sall.y;
-    }
-    if (ok && nt[t] > 0) ok = wwait(sm.o_done[t][(nt[t] - 1) % kStages], ((nt[t] - 1) / kStages) & 1);
-    // ---- out = O vref / l, after every role is done (the bad-block flag is final) ----
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const bool good = ok && sm.abort == 0 && sm.bad == 0;
-    const float inv = vref / l_run;
-    // (clamped: a cached f16 value may have been rounded up past 65504)
-    // The rows go out through shared memory (the K ring, idle now), so that each store
-    // instruction of a warp writes whole rows.  Row r's 16-byte chunk c sits at chunk
-    // c ^ (r % CH) of its 2 D-byte staging row, so that neither the writes nor the reads
-    // collide in a bank much.
-    static_assert(kStages * kKeys >= 8 * 32, "the K ring holds a staging row per thread");
-    const uint32_t stage = smem_addr(sm.k[0]) + static_cast<uint32_t>(warp) * 32 * D * 2;
-    const int rw = r & 31;
+        __syncwarp();
+        uint4 x[8];
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += 32) {
-      float o[32];
-      if (nt[t] > 0 && sm.abort == 0) tmem_ld32(tl + kColO + c0, o);  // (warp-uniform)
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (good && nt[t] > 0) {
-          w.x = pack2_sat<T>(o[8 * cc + 0] * inv, o[8 * cc + 1] * inv);
-          w.y = pack2_sat<T>(o[8 * cc + 2] * inv, o[8 * cc + 3] * inv);
-          w.z = pack2_sat<T>(o[8 * cc + 4] * inv, o[8 * cc + 5] * inv);
-          w.w = pack2_sat<T>(o[8 * cc + 6] * inv, o[8 * cc + 7] * inv);
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          x[i] = ld_shared16(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
         }
-        const int ch = c0 / 8 + cc;  // 16-byte chunk of the row
-        st_shared16(stage + rw * D * 2 + ((ch ^ (rw & (CH - 1))) << 4), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at[i] >= 0) *reinterpret_cast<uint4*>(to + at[i] + c0) = x[i];
+        __syncwarp();  // the reads before the next columns' stores
       }
+      // the O loads before this warp's next P, which lets the next item's P V overwrite O
+      tc_fence_before();
     }
-    __syncwarp();
-    // piece i of the warp: row i / CH, chunk i % CH
-    const int ch = lane % CH;
-    const size_t row0 = static_cast<size_t>(qs + tok0 + t * tpt) * p.num_q_heads + g * G;
-#pragma unroll 8
-    for (int rr = lane / CH; rr < 32; rr += 32 / CH) {
-      const int rrow = (r - rw) + rr;  // the row in the tile: token tk of it, head rrow % G
-      const int tk = static_cast<int>((rrow * p.group_magic) >> 16);
-      if (tk < tpt && tok0 + t * tpt + tk < qlen)
-        reinterpret_cast<uint4*>(outp + (row0 + static_cast<size_t>(tk) * (p.num_q_heads - G) + rrow) * D)[ch] =
-            ld_shared16(stage + rr * D * 2 + ((ch ^ (rr & (CH - 1))) << 4));
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0 && sm.bad) atomicOr(p.err, kErrBadBlock);
-    return;
   }
-  // the other roles: the two CTA-wide barriers of the softmax epilogue
   tc_fence_before();
-  __syncthreads();
   __syncthreads();
   if (warp == kMmaWarp + 1) {
     tc_fence_after();
@@ -706,13 +927,14 @@ int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
   auto* kern = prefill_fp8_block_kernel<D, T>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return -3;
   cudaLaunchConfig_t cfg = {};
-  const int per_cta = kTiles * prm.tpt;
-  const int ncb = (max_query_len + per_cta - 1) / per_cta;
+  // query blocks, whatever the lengths are: a part of one per sequence beyond the whole ones
+  const int per_item = kTiles * prm.tpt;
   Params q = prm;
-  q.ncb = ncb;
-  // x: a block within its half (the later half has ceil(ncb / 2)), y: sequence,
-  // z: half x kv head
-  cfg.gridDim = dim3((ncb + 1) / 2, prm.num_seqs, 2 * prm.num_kv_heads);
+  q.max_blocks = (max_query_len + per_item - 1) / per_item;
+  const long long blocks = std::min(static_cast<long long>(prm.num_tokens / per_item) + prm.num_seqs,
+                                    static_cast<long long>(prm.num_seqs) * q.max_blocks);
+  if (blocks * prm.num_kv_heads > 0x7fffffffLL) return -1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * prm.num_kv_heads));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
