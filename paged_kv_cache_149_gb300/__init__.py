@@ -697,7 +697,71 @@ def swap_blocks_int4(src, dst, block_mapping, stream=None, device=None):
     _check(st, "pa_swap_blocks_int4")
 
 
-@_on_first
+# ---- FP8 blocks with a scale per (block, kv head), and the step's bookkeeping ----
+# A serving step makes these calls back to back, several of them shorter on the GPU than in
+# Python, so their checks touch each tensor as little as possible.
+
+def _ptr(t, name, dtype, dev):
+    """Address of a contiguous tensor of `dtype` on CUDA device number `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(t, name, (dtype,), dev)
+
+
+def _codes_ptr(t, name, dev):
+    """The same of E4M3 codes (uint8 or float8_e4m3fn)."""
+    import torch
+    if (t.dtype is torch.uint8 or t.dtype is torch.float8_e4m3fn) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(t, name, (torch.uint8, torch.float8_e4m3fn), dev)
+
+
+def _device_of(t, name):
+    """The CUDA device number of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _refuse(t, name, dtypes, dev):
+    _need(t.is_cuda, f"{name} must be a CUDA tensor")
+    _need(t.get_device() == dev, f"{name} is on another device than the call's first tensor")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+
+
+def _on_its_device(fn):
+    """Decorator: run the call with the device of its first tensor current."""
+    @functools.wraps(fn)
+    def wrapped(t, *args, **kw):
+        import torch
+        first = t[0] if isinstance(t, (tuple, list)) else t
+        dev = first.get_device()
+        if dev < 0 or dev == torch._C._cuda_getDevice():
+            return fn(t, *args, **kw)
+        with torch.cuda.device(dev):
+            return fn(t, *args, **kw)
+    return wrapped
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _block_scaled(k_cache, v_cache, k_scales, v_scales, d):
+    """(num_blocks, num_kv_heads, block_size) of the caches, checked against each other."""
+    nb, hkv, bs, d2 = shape = k_cache.shape
+    _need(d2 == d and v_cache.shape == shape, "shape mismatch")
+    if k_scales.shape != (nb, hkv) or v_scales.shape != (nb, hkv):
+        raise ValueError("k, v: codes [NB, Hkv, B, d] and scales [NB, Hkv]")
+    return nb, hkv, bs
+
+
+@_on_its_device
 def build_step(query_lens, context_lens, free_blocks, free_start, block_tables, block_size,
                num_blocks, slot_mapping, query_start=None, free_next=None, stream=None, plan=False):
     """Block tables and slots of one step from request lengths, on the GPU: request s has
@@ -706,46 +770,41 @@ def build_step(query_lens, context_lens, free_blocks, free_start, block_tables, 
     slot_mapping gets the slot of every new token (-1 past the last one); returns
     (query_start [num_seqs + 1], free_next [1]).  A step that lacks blocks or slots changes
     no table, sets every slot to -1 and a device error bit.  plan=True returns a Launch whose
-    runs return query_start (free_next must then be given)."""
+    runs return query_start (query_start and free_next must then be given)."""
     import torch
-    n = query_lens.shape[0]
-    _need(query_lens.dim() == 1 and context_lens.shape == (n,), "query_lens and context_lens must be [num_seqs]")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
-    _need(free_blocks.dim() == 1 and slot_mapping.dim() == 1, "free_blocks and slot_mapping must be 1-D")
+    dev, i32 = _device_of(query_lens, "query_lens"), torch.int32
+    n, = query_lens.shape
+    tn, width = block_tables.shape
+    _need(context_lens.shape == (n,), "query_lens and context_lens must be [num_seqs]")
+    _need(tn == n, "block_tables must be [num_seqs, T]")
+    nfree, = free_blocks.shape
+    slots, = slot_mapping.shape
     _need(free_start.numel() == 1, "free_start must hold one value")
     if query_start is None or free_next is None:
         _need(not plan, "a planned build_step needs query_start and free_next")
         with torch.cuda.stream(stream):  # (allocated for the stream that writes them)
             if query_start is None:
-                query_start = torch.empty(n + 1, dtype=torch.int32, device=query_lens.device)
+                query_start = torch.empty(n + 1, dtype=i32, device=query_lens.device)
             if free_next is None:
-                free_next = torch.empty(1, dtype=torch.int32, device=query_lens.device)
+                free_next = torch.empty(1, dtype=i32, device=query_lens.device)
     _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
     _need(free_next.numel() == 1, "free_next must hold one value")
-    i32 = torch.int32
-    args = (_dev(query_lens, "query_lens", i32), _dev(context_lens, "context_lens", i32), n,
-            _dev(free_blocks, "free_blocks", i32), free_blocks.shape[0],
-            _dev(free_start, "free_start", i32), _dev(block_tables, "block_tables", i32),
-            block_tables.shape[1], int(block_size), int(num_blocks),
-            _dev(slot_mapping, "slot_mapping", torch.int64), slot_mapping.shape[0],
-            _dev(query_start, "query_start", i32), _dev(free_next, "free_next", i32))
+    args = (_ptr(query_lens, "query_lens", i32, dev), _ptr(context_lens, "context_lens", i32, dev),
+            n, _ptr(free_blocks, "free_blocks", i32, dev), nfree,
+            _ptr(free_start, "free_start", i32, dev), _ptr(block_tables, "block_tables", i32, dev),
+            width, int(block_size), int(num_blocks), _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
+            slots, _ptr(query_start, "query_start", i32, dev), _ptr(free_next, "free_next", i32, dev))
     if plan:
         return Launch("pa_build_step", args, query_start,
                       keep=(query_lens, context_lens, free_blocks, free_start, block_tables,
                             slot_mapping, free_next))
-    _check(lib().pa_build_step(*args, _stream_ptr(stream, query_lens.device)), "pa_build_step")
+    st = lib().pa_build_step(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_build_step")
     return query_start, free_next
 
 
-def _fp8_block_cache(codes, scales, name):
-    """(codes, scales) addresses of one cache of FP8 blocks with block scales."""
-    import torch
-    if not (codes.dim() == 4 and scales.shape == codes.shape[:2]):
-        raise ValueError(f"{name}: codes [NB, Hkv, B, d] and scales [NB, Hkv]")
-    return _fp8_cache(codes, name + "_cache"), _dev(scales, name + "_scales", torch.float32)
-
-
-@_on_first
+@_on_its_device
 def append_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                      query_start, stream=None, plan=False):
     """Cache write of FP8 blocks with a scale per (block, kv head): sequence s's rows
@@ -754,103 +813,114 @@ def append_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tab
     its rows; where a new row raises it, the block's earlier rows are requantised.  Rows
     behind the last sequence are not read.  plan=True returns a Launch instead of writing."""
     import torch
-    ntok, hkv, d = key.shape
-    nb, hkv2, bs, d2 = k_cache.shape
-    n = context_lens.shape[0]
-    _need(value.shape == key.shape and v_cache.shape == k_cache.shape, "shape mismatch")
-    _need(hkv == hkv2 and d == d2, "shape mismatch")
-    _need(key.dtype == value.dtype, "dtype mismatch")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    dev, i32, dt, f32 = _device_of(key, "key"), torch.int32, key.dtype, torch.float32
+    ntok, heads, d = shape = key.shape
+    n, width = block_tables.shape
+    nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
+    _need(heads == hkv and value.shape == shape, "shape mismatch")
+    _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
     _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
-    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
-    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
-    args = (_dev(key, "key"), _dev(value, "value"), kc, vc, ks, vs,
-            _dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-            _dev(context_lens, "context_lens", torch.int32),
-            _dev(query_start, "query_start", torch.int32), n, ntok, nb, hkv, d, bs,
-            _dtype_code(key))
+    args = (_ptr(key, "key", dt, dev), _ptr(value, "value", dt, dev),
+            _codes_ptr(k_cache, "k_cache", dev), _codes_ptr(v_cache, "v_cache", dev),
+            _ptr(k_scales, "k_scales", f32, dev), _ptr(v_scales, "v_scales", f32, dev),
+            _ptr(block_tables, "block_tables", i32, dev), width,
+            _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
+            n, ntok, nb, hkv, d, bs, _dtype_code(key))
     if plan:
         return Launch("pa_append_fp8_block", args, k_cache,
                       keep=(key, value, v_cache, k_scales, v_scales, block_tables, context_lens,
                             query_start))
-    _check(lib().pa_append_fp8_block(*args, _stream_ptr(stream, key.device)), "pa_append_fp8_block")
+    st = lib().pa_append_fp8_block(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_append_fp8_block")
 
 
-@_on_first
+@_on_its_device
 def decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
                      out=None, workspace=None, stream=None, plan=False):
     """Paged decode over FP8 blocks with a scale per (block, kv head) (codes [NB, Hkv, B, d],
     scales [NB, Hkv] float32); q and out are fp16 or bf16.  plan=True returns a Launch
     instead of launching."""
     import torch
-    n, hq, d = q.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    _need(v_cache.shape == k_cache.shape and d == d2, "shape mismatch")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    dev, i32, dt, f32 = _device_of(q, "q"), torch.int32, q.dtype, torch.float32
+    n, hq, d = shape = q.shape
+    tn, width = block_tables.shape
+    nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
+    _need(tn == n, "block_tables must be [num_seqs, T]")
     _need(context_lens.shape == (n,), "context_lens must be [num_seqs]")
-    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
-    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
     if out is None:
         out = torch.empty_like(q)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    elif out.shape != shape or out.dtype is not dt:
+        raise ValueError("out must match q")
     if workspace is None:
         workspace = _scratch(hq, hkv, d, q.device, stream)
-    args = (_dev(q, "q"), kc, vc, ks, vs, _dev(block_tables, "block_tables", torch.int32),
-            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), n, hq, hkv, d,
-            bs, nb, float(scale), _dev(out, "out"), _dev(workspace, "workspace"),
+    args = (_ptr(q, "q", dt, dev), _codes_ptr(k_cache, "k_cache", dev),
+            _codes_ptr(v_cache, "v_cache", dev), _ptr(k_scales, "k_scales", f32, dev),
+            _ptr(v_scales, "v_scales", f32, dev), _ptr(block_tables, "block_tables", i32, dev),
+            width, _ptr(context_lens, "context_lens", i32, dev), n, hq, hkv, d, bs, nb, float(scale),
+            _ptr(out, "out", dt, dev), _ptr(workspace, "workspace", workspace.dtype, dev),
             workspace.numel() * workspace.element_size(), _dtype_code(q))
     if plan:
         return Launch("pa_decode_fp8_block", args, out,
                       keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                             workspace))
-    _check(lib().pa_decode_fp8_block(*args, _stream_ptr(stream, q.device)), "pa_decode_fp8_block")
+    st = lib().pa_decode_fp8_block(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_decode_fp8_block")
     return out
 
 
-@_on_first
+@_on_its_device
 def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                       query_start, scale, max_query_len, out=None, stream=None, plan=False):
     """prefill over FP8 blocks with a scale per (block, kv head): causal attention of each
     sequence's newest tokens over its paged context; the tokens' own rows must already be in
-    the cache (append_fp8_block).  plan=True returns a Launch instead of launching."""
+    the cache (append_fp8_block).  scale must be positive.  plan=True returns a Launch
+    instead of launching."""
     import torch
-    ntok, hq, d = q.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    n = context_lens.shape[0]
-    _need(v_cache.shape == k_cache.shape and d == d2, "shape mismatch")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == n, "block_tables must be [num_seqs, T]")
+    dev, i32, dt, f32 = _device_of(q, "q"), torch.int32, q.dtype, torch.float32
+    ntok, hq, d = shape = q.shape
+    n, width = block_tables.shape
+    nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
+    _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
     _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
-    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
-    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
     if out is None:
         out = torch.empty_like(q)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
-    args = (_dev(q, "q"), kc, vc, ks, vs, _dev(block_tables, "block_tables", torch.int32),
-            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32),
-            _dev(query_start, "query_start", torch.int32), n, ntok, int(max_query_len), hq, hkv, d,
-            bs, nb, float(scale), _dev(out, "out"), _dtype_code(q))
+    elif out.shape != shape or out.dtype is not dt:
+        raise ValueError("out must match q")
+    args = (_ptr(q, "q", dt, dev), _codes_ptr(k_cache, "k_cache", dev),
+            _codes_ptr(v_cache, "v_cache", dev), _ptr(k_scales, "k_scales", f32, dev),
+            _ptr(v_scales, "v_scales", f32, dev), _ptr(block_tables, "block_tables", i32, dev),
+            width, _ptr(context_lens, "context_lens", i32, dev),
+            _ptr(query_start, "query_start", i32, dev), n, ntok, int(max_query_len), hq, hkv, d, bs, nb,
+            float(scale), _ptr(out, "out", dt, dev), _dtype_code(q))
     if plan:
         return Launch("pa_prefill_fp8_block", args, out,
                       keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                             query_start))
-    _check(lib().pa_prefill_fp8_block(*args, _stream_ptr(stream, q.device)), "pa_prefill_fp8_block")
+    st = lib().pa_prefill_fp8_block(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_prefill_fp8_block")
     return out
 
 
-@_on_first
+@_on_its_device
 def copy_blocks_fp8_block(k_cache, v_cache, k_scales, v_scales, block_mapping, stream=None):
     """copy_blocks for FP8 blocks with block scales: codes and scales of each (src, dst) pair
     in one launch."""
     import torch
-    nb, hkv, bs, d = k_cache.shape
-    _need(v_cache.shape == k_cache.shape, "shape mismatch")
-    _need(block_mapping.dim() == 2 and block_mapping.shape[1] == 2, "block_mapping must be [n, 2]")
-    kc, ks = _fp8_block_cache(k_cache, k_scales, "k")
-    vc, vs = _fp8_block_cache(v_cache, v_scales, "v")
+    dev, f32 = _device_of(k_cache, "k_cache"), torch.float32
+    d = k_cache.shape[3]
+    nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
+    pairs, two = block_mapping.shape
+    _need(two == 2, "block_mapping must be [n, 2]")
     st = lib().pa_copy_blocks_fp8_block(
-        kc, vc, ks, vs, _dev(block_mapping, "block_mapping", torch.int32), block_mapping.shape[0],
-        nb, hkv, d, bs, _stream_ptr(stream, k_cache.device))
-    _check(st, "pa_copy_blocks_fp8_block")
+        _codes_ptr(k_cache, "k_cache", dev), _codes_ptr(v_cache, "v_cache", dev),
+        _ptr(k_scales, "k_scales", f32, dev), _ptr(v_scales, "v_scales", f32, dev),
+        _ptr(block_mapping, "block_mapping", torch.int32, dev), pairs, nb, hkv, d, bs,
+        _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_copy_blocks_fp8_block")
 
 
 @_runs_on(_pool_device)

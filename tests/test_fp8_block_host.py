@@ -89,8 +89,8 @@ def test_copy_and_swap_refusals(libpa):
 
 @pytest.fixture
 def cpu_marshal(libpa, monkeypatch):
-    """The device checks replaced by address lookups: marshalling on CPU tensors."""
-    monkeypatch.setattr(libpa, "_dev", lambda t, name, dtype=None: t.data_ptr())
+    """CPU tensors pass for those of device -1: marshalling without a GPU."""
+    monkeypatch.setattr(libpa, "_device_of", lambda t, name: -1)
     monkeypatch.setattr(libpa, "make_workspace", lambda *a: torch.empty(256, dtype=torch.uint8))
     return libpa
 
@@ -125,19 +125,53 @@ def test_shape_and_type_checks_name_the_argument(cpu_marshal):
     kc, vc, ks, vs = cache()
     tables, lens = torch.zeros(N, T, dtype=torch.int32), torch.ones(N, dtype=torch.int32)
     q = torch.zeros(N, HQ, D, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="k: codes"):
+    with pytest.raises(ValueError, match=r"scales \[NB, Hkv\]"):
         pa.decode_fp8_block(q, kc, vc, ks[:, :1], vs, tables, lens, 0.1)
-    with pytest.raises(ValueError, match="must hold E4M3"):
+    with pytest.raises(ValueError, match="k_cache must be a CUDA tensor"):
         pa.decode_fp8_block(q, kc.float(), vc, ks, vs, tables, lens, 0.1)
+    with pytest.raises(ValueError, match="tables must be a CUDA tensor"):
+        pa.decode_fp8_block(q, kc, vc, ks, vs, tables.long(), lens, 0.1)
     with pytest.raises(ValueError, match="out must match q"):
         pa.decode_fp8_block(q, kc, vc, ks, vs, tables, lens, 0.1, out=q.float())
     rows = torch.zeros(N, HKV, D, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="query_start must be"):
         pa.append_fp8_block(rows, rows, kc, vc, ks, vs, tables, lens, lens)
-    with pytest.raises(ValueError, match="dtype mismatch"):
-        pa.append_fp8_block(rows, rows.half(), kc, vc, ks, vs, tables, lens, torch.zeros(N + 1))
+    start = torch.zeros(N + 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="value must be"):
+        pa.append_fp8_block(rows, rows.half(), kc, vc, ks, vs, tables, lens, start)
+    with pytest.raises(ValueError, match="value must be"):
+        pa.append_fp8_block(rows, rows.transpose(0, 1).contiguous().transpose(0, 1), kc, vc, ks, vs,
+                            tables, lens, start)
     with pytest.raises(TypeError, match="unsupported dtype"):
-        pa.append_fp8_block(rows.float(), rows.float(), kc, vc, ks, vs, tables, lens, torch.zeros(N + 1))
+        pa.append_fp8_block(rows.float(), rows.float(), kc, vc, ks, vs, tables, lens, start)
+
+
+def test_tensors_of_another_device_are_refused(libpa):
+    """Every tensor must be on the device of the call's first one, and that a CUDA device."""
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        libpa.decode_fp8_block(torch.zeros(N, HQ, D, dtype=torch.float16), *cache(),
+                               torch.zeros(N, T, dtype=torch.int32), torch.ones(N, dtype=torch.int32), 0.1)
+
+    class On:
+        def __init__(self, dev, dtype=torch.int32):
+            self.dev, self.dtype, self.is_cuda = dev, dtype, dev >= 0
+
+        def get_device(self):
+            return self.dev
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return P
+
+    assert libpa._ptr(On(1), "lens", torch.int32, 1) == P
+    assert libpa._codes_ptr(On(0, torch.uint8), "k_cache", 0) == P
+    for t, match in ((On(0), "another device"), (On(-1), "CUDA tensor"), (On(1, torch.int64), "must be torch.int32, got")):
+        with pytest.raises(ValueError, match=match):
+            libpa._ptr(t, "lens", torch.int32, 1)
+    with pytest.raises(ValueError, match="uint8 or torch.float8_e4m3fn, got"):
+        libpa._codes_ptr(On(1, torch.float16), "k_cache", 1)
 
 
 def test_calls_make_their_tensors_device_current(libpa):
