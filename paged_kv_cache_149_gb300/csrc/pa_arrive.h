@@ -45,4 +45,28 @@ PA_HOST_DEVICE int arrive_count(unsigned long long* ctr, unsigned long long tag,
   return -1;
 }
 
+// The same with an atomic add once the counter carries this call's tag, which only arrivals
+// of the pair's own pieces put there.  Compare-and-swaps that many arrivals make at once fail
+// for all but one, a round trip to the L2 for each; adds all succeed.  One sequence of 512
+// tokens with 8 kv heads, whose 16 pieces a head all end together: 67 us with swaps alone.
+// A counter that turns out to hold a third call's tag is left to the loop above.
+// add(ptr) adds one and returns the old value; store(ptr, value) writes the counter.
+#if defined(__CUDACC__)
+#pragma nv_exec_check_disable
+#endif
+template <class Cas, class Load, class Add, class Store>
+PA_HOST_DEVICE int arrive_add(unsigned long long* ctr, unsigned long long tag, int n, Cas cas,
+                              Load load, Add add, Store store) {
+  unsigned long long cur = load(ctr);
+  if ((cur >> 24) != tag) {
+    const unsigned long long prev = cas(ctr, cur, n > 1 ? (tag << 24) + 1 : tag << 24);
+    if (prev == cur) return 1;
+    if ((prev >> 24) != tag) return arrive_count(ctr, tag, n, cas, load);
+  }
+  const int count = static_cast<int>(add(ctr) & kArriveCountMask) + 1;
+  if (count < n) return count;
+  store(ctr, tag << 24);
+  return n;
+}
+
 }  // namespace pa

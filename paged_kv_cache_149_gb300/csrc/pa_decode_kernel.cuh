@@ -16,7 +16,8 @@
 //   ns(s) units of 16 tokens (32 over FP8 / INT4 blocks) x gs pairs (a "stage" is one
 //   unit of one pair: its K rows and V rows), plus a fixed charge.  The batch's stages, in
 //   (family, unit, pair) order, are cut into gridDim.x equal contiguous shares, one per
-//   persistent CTA (one per SM).
+//   persistent CTA (one per SM); over FP8 blocks with block scales into fewer where few
+//   sequences would be cut into many pieces.
 // * Warp w of a CTA works on pair w / P of every family (P = 8 / gs warps per pair, each
 //   taking every P-th unit).  With 8 or more kv heads (gs = 8) a warp owns one kv head
 //   outright: it streams its pair's stages straight across family boundaries and never
@@ -162,6 +163,7 @@ struct Params {
   int max_blocks_per_seq, block_size, log2_block, num_blocks, max_ctx;
   int log2_stage;  // tokens per stage: 16 (16-bit blocks) or 32 (FP8 blocks)
   int seg_cost;    // stage units charged per family on top of its stages
+  float piece_cost;  // FB: piece time / step time x steps per unit (see the kernel's shares)
   float scale_log2;
   float out_scale;  // FP8 blocks: v_scale, applied to every output row (else 1)
   float k_quant, v_quant;  // FP8 blocks: k_scale, v_scale for the fused step's newest rows
@@ -492,9 +494,7 @@ __device__ __forceinline__ CutPiece cut_piece(const Fam& f, int pi, const PairHe
 }
 
 // Count one piece in at a pair's counter (pa_arrive.h): the count this arrival makes
-// (n: it completed the pair, and the counter is back at zero), or -1 if it gave up.  The
-// loop retries only when another arrival changed the counter in between, so it ends after
-// at most one try per piece.
+// (n: it completed the pair, and the counter is back at zero), or -1 if it gave up.
 struct DeviceCas {
   __device__ unsigned long long operator()(unsigned long long* a, unsigned long long e,
                                            unsigned long long d) const {
@@ -506,9 +506,17 @@ struct DeviceLoad {
     return *reinterpret_cast<volatile unsigned long long*>(a);
   }
 };
+struct DeviceAdd {
+  __device__ unsigned long long operator()(unsigned long long* a) const { return atomicAdd(a, 1ull); }
+};
+struct DeviceStore {
+  __device__ void operator()(unsigned long long* a, unsigned long long v) const {
+    *reinterpret_cast<volatile unsigned long long*>(a) = v;
+  }
+};
 
 __device__ __forceinline__ int arrive(unsigned long long* ctr, unsigned long long epoch, int n) {
-  return arrive_count(ctr, epoch, n, DeviceCas(), DeviceLoad());
+  return arrive_add(ctr, epoch, n, DeviceCas(), DeviceLoad(), DeviceAdd(), DeviceStore());
 }
 
 // Two output values of a K/V format.  With block scales a cached value may round up past f16's
@@ -566,6 +574,68 @@ __device__ void merge_pieces(const Params& p, int pi, int c, int first_slot, int
     }
     *reinterpret_cast<uint2*>(out_rows + h * D + d4) = packed;
   }
+}
+
+// merge_pieces by the P warps of a pair (gthreads threads, `sync` their barrier) with every
+// piece's (m, l) staged in `ml` (shared memory for `room` entries): all of them in one round
+// of loads, the weights by one thread per head, and the O of several pieces in flight.  The
+// same sums in the same order.  Returns false, having done nothing, when `ml` is too small.
+// One sequence of 11856 tokens with one kv head and 16 query heads, 152 pieces: 82 us, 115 us
+// with merge_pieces, whose loads follow one another piece by piece.
+template <int D, typename T, int KV, class Sync>
+__device__ bool merge_pieces_group(const Params& p, int pi, const CutPiece& cp, T* out_rows, float2* ml,
+                                   int room, int gt, int gthreads, Sync sync) {
+  constexpr int C4 = D / 4;  // 4-float chunks per head row
+  const int hpp = p.heads_per_pair, np = cp.c_last - cp.c_first + 1, nh = cp.nh;
+  if (np * nh > room) return false;
+  auto piece_of = [&](int i) {
+    return (static_cast<size_t>(cp.c_first + i) * 2 + (i == 0 ? cp.first_slot : 0)) * p.gs + pi;
+  };
+  sync();  // (the memory's last use is over)
+  for (int i = gt; i < np * nh; i += gthreads) {
+    const float* src = p.part_ml + (piece_of(i / nh) * hpp + i % nh) * 2;
+    ml[i] = make_float2(__ldcg(src), __ldcg(src + 1));
+  }
+  sync();
+  for (int h = gt; h < nh; h += gthreads) {
+    float M = -INFINITY;
+    bool bad = false;
+    for (int i = 0; i < np; ++i) {
+      M = fmaxf(M, ml[i * nh + h].x);
+      bad |= ml[i * nh + h].y < 0.f;
+    }
+    float L = 0.f;
+    for (int i = 0; i < np; ++i) {
+      float2 v = ml[i * nh + h];
+      const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+      L = fmaf(v.y, w, L);
+      ml[i * nh + h].x = w;
+    }
+    ml[h].y = bad ? -1.f : L;  // (read back below only through this slot)
+  }
+  sync();
+  for (int idx = gt; idx < nh * C4; idx += gthreads) {
+    const int h = idx / C4, d4 = (idx % C4) * 4;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+    for (int i = 0; i < np; ++i) {
+      const float w = ml[i * nh + h].x;
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_acc + (piece_of(i) * hpp + h) * D + d4));
+      O.x = fmaf(a.x, w, O.x);
+      O.y = fmaf(a.y, w, O.y);
+      O.z = fmaf(a.z, w, O.z);
+      O.w = fmaf(a.w, w, O.w);
+    }
+    const float L = ml[h].y;
+    uint2 packed = make_uint2(0u, 0u);
+    if (!(L < 0.f)) {  // (a NaN sum is no bad block: NaN out)
+      const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
+      packed.x = pack_out<T, KV>(O.x * inv, O.y * inv);
+      packed.y = pack_out<T, KV>(O.z * inv, O.w * inv);
+    }
+    *reinterpret_cast<uint2*>(out_rows + h * D + d4) = packed;
+  }
+  return true;
 }
 
 // Wait for the phase of `bar` with parity `parity`, bounded by kWaitLimitNs.
@@ -677,7 +747,7 @@ __device__ bool merge_staged_once(const Params& p, int pi, const CutPiece& job0,
       }
       const float L = ml[moff + h].y;
       uint2 packed = make_uint2(0u, 0u);
-      if (L >= 0.f) {
+      if (!(L < 0.f)) {
         const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
         packed.x = pack_out<T, KV>(O.x * inv, O.y * inv);
         packed.y = pack_out<T, KV>(O.z * inv, O.w * inv);
@@ -848,7 +918,7 @@ __device__ bool merge_staged_chunked(const Params& p, int pi, const CutPiece& jo
       const int h = idx / C4, d4 = (idx % C4) * 4;
       const float L = ml[moff + h].y;
       uint2 packed = make_uint2(0u, 0u);
-      if (L >= 0.f) {
+      if (!(L < 0.f)) {
         const float inv = KV != kKv16 ? p.out_scale / L : 1.f / L;
         packed.x = pack_out<T, KV>(O[it].x * inv, O[it].y * inv);
         packed.y = pack_out<T, KV>(O[it].z * inv, O[it].w * inv);
@@ -880,6 +950,7 @@ struct Smem {
   alignas(16) float xo[kWarps][4][D];  // per-warp O rows, 4 heads per exchange round
   float xm[kWarps][kMaxHeads], xl[kWarps][kMaxHeads];
   long long scan[kWarps];
+  int longest[kWarps];  // FB: most units of a pair
   long long start_pre;
   int start_s;
   int last[kWarps];  // per pair group: this CTA's arrival completed the pair
@@ -1042,10 +1113,16 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   const int per = (p.num_seqs + kThreads - 1) / kThreads;
   const int sa = min(p.num_seqs, tid * per), sb = min(p.num_seqs, sa + per);
   long long mine = 0;
-  for (int s = sa; s < sb; ++s)
-    mine += static_cast<long long>(p.ngroups) *
-            (static_cast<long long>(pair_stages(__ldg(p.context_lens + s), p)) * p.gs +
-             p.seg_cost);
+  int longest_mine = 0;
+  for (int s = sa; s < sb; ++s) {
+    const int ns = pair_stages(__ldg(p.context_lens + s), p);
+    longest_mine = max(longest_mine, ns);
+    mine += static_cast<long long>(p.ngroups) * (static_cast<long long>(ns) * p.gs + p.seg_cost);
+  }
+  if constexpr (FB) {
+    longest_mine = __reduce_max_sync(0xffffffffu, longest_mine);
+    if (lane == 0) sm.longest[warp] = longest_mine;
+  }
   long long incl = mine;  // inclusive scan of `mine` over the block
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1060,8 +1137,24 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     W += sm.scan[w];
   }
   const long long excl = before + incl - mine;
-  const int G = gridDim.x;
+  int G = gridDim.x;
   const int c = blockIdx.x;
+  if constexpr (FB) {
+    // Few shares for few long sequences.  A sequence of n steps (a step: one stage for each
+    // of the eight warps) in shares of R steps takes about R step times and then the merge of
+    // n / R pieces by one CTA, least at R = sqrt(n x piece time / step time); smaller shares
+    // than one step would leave pieces of warps without a stage.  Batches whose equal shares
+    // are larger than that are cut as ever.  One sequence of 512 / 4096 / 16384 tokens, 8 kv
+    // heads of 128, 4 query heads each: 12.9 / 22.6 / 36.1 us against 14.8 / 47.5 / 56.1 us
+    // with shares of one step at least (and 31.1 / 38.3 us at 512 / 4096, head dim 64, with
+    // any); 8 sequences of 8-32 K tokens are cut as before.
+    int longest = 0;
+    for (int w = 0; w < kWarps; ++w) longest = max(longest, sm.longest[w]);
+    const float steps = sqrtf(static_cast<float>(longest) * p.piece_cost);
+    const long long share = kWarps * static_cast<long long>(fmaxf(steps, 1.f));
+    G = static_cast<int>(min(static_cast<long long>(G), max(1ll, W / share)));
+    if (c >= G) return;  // (uniform over the CTA)
+  }
   long long w0, w1;
   share_of(c, W, G, w0, w1);
   if (w0 < w1 && excl <= w0 && w0 < excl + mine) {
@@ -2009,6 +2102,12 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       const CutPiece& cp = k == 0 ? cut_a : cut_b;
       T* out_rows =
           reinterpret_cast<T*>(p.out) + (static_cast<size_t>(cp.s) * p.num_q_heads + cp.h0) * D;
+      // (P > 1: the rings of the pair's warps are idle now and lie side by side)
+      if (P > 1 && merge_pieces_group<D, T, KV>(p, pi, cp, out_rows,
+                                                reinterpret_cast<float2*>(sm.ring[pi * P][0]),
+                                                P * R * G_::kStageBytes / static_cast<int>(sizeof(float2)),
+                                                gt, gthreads, gsync))
+        continue;
       merge_pieces<D, T, KV>(p, pi, cp.c_first, cp.first_slot, cp.c_last, cp.nh, out_rows, gt,
                          gthreads);
     }
