@@ -511,7 +511,7 @@ int prefill_call(const void* q, const void* k_cache, const void* v_cache, const 
   a.scale = scale;
   a.bf16 = dtype == PA_BF16;
   a.err = di.err;
-  return fp8_block ? pa::prefill_fp8_block_launch(a, num_tokens, k_scales, v_scales, stream)
+  return fp8_block ? pa::prefill_fp8_block_launch(a, num_tokens, k_scales, v_scales, di.sm_count, stream)
                    : pa::prefill_launch(a, stream);
 }
 

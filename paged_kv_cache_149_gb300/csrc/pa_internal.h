@@ -60,7 +60,7 @@ struct PrefillArgs {
 int prefill_launch(const PrefillArgs& a, cudaStream_t stream);
 // The same over FP8 blocks with block scales [NB][Hkv]; q has num_tokens rows.
 int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* k_scales,
-                             const float* v_scales, cudaStream_t stream);
+                             const float* v_scales, int sm_count, cudaStream_t stream);
 // q as [tokens][Hq][d] 16-bit for TMA loads of whole 128-row query tiles; false when the
 // group does not divide 128 or the driver's encoder is missing or rejects the tensor.
 bool q_tile_map(CUtensorMap* map, const void* q, int hq, int d, int g, long long tokens);

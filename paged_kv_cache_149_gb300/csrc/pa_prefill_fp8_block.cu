@@ -23,13 +23,14 @@
 // that have not started (cluster launch control), so the SMs balance themselves, and its roles
 // go from item to item at their own pace: the next item's codes, K, V and q arrive while this
 // one's last tiles are multiplied and written out.  (One CTA per item spent about 13600 cycles
-// of its 34000, 8 prompts of 2048 tokens, on starting up and writing out alone.)
+// of its 34000, 8 prompts of 2048 tokens, on starting up and writing out alone.)  A call with few
+// items makes them one query tile each (see the launch).
 // * A query tile's rows are (token, query head of the kv head) pairs, 128 / G tokens x G
 //   heads; both tiles of the CTA share the key tiles (64 keys each).
 // * Two producer warps (K, V) look blocks and scales up a tile ahead and copy whole blocks of
 //   codes by TMA into two buffers each.
 // * Eight widening warps (four for K, four for V) turn codes into f16 in the swizzled layout
-//   that the tcgen05 descriptors read, into a ring of four K and four V tiles.  Rows past the
+//   that the tcgen05 descriptors read, into rings of kStages K and V tiles.  Rows past the
 //   context become zeros (what lies there is not used).
 // * An MMA warp per query tile: S = Q K^T into tensor memory (two buffers of 64 columns,
 //   alternate key tiles), P V from the P that the tile's softmax leaves over the first half of
@@ -89,7 +90,8 @@ struct Params {
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group, tpt;  // tpt = tokens per query tile
   int max_blocks_per_seq, block_size, log2_block, num_blocks;
   uint32_t group_magic;  // ceil(2^16 / G): r / G = r * group_magic >> 16 for r < 128
-  int max_blocks;  // query blocks (of kTiles x tpt tokens) taken of a sequence at most
+  int tiles;       // query tiles of an item: kTiles, or 1 where that fills the SMs better
+  int max_blocks;  // query blocks (of tiles x tpt tokens) taken of a sequence at most
   float scale_log2;
   unsigned* err;
 };
@@ -98,14 +100,15 @@ struct Params {
 struct Item {
   int run;  // 0: no more items, 1: attend, 2: an impossible sequence, zeros
   int g;    // kv head
-  int qs, qlen, ctx, tok0;  // the sequence's first row of q, rows, context; the item's first token
+  int qs, qlen, ctx;  // the sequence's first row of q, rows, context
+  int tok0, end;      // the item's tokens of the sequence
   int s;
   int bad;  // a block id of its keys is out of range
 };
 
 // Keys that query tile t of an item needs, in tiles: up to the position of its last token.
 __device__ __forceinline__ int key_tiles(const Item& it, int t, int tpt) {
-  const int ntok = min(tpt, it.qlen - (it.tok0 + t * tpt));
+  const int ntok = min(tpt, it.end - (it.tok0 + t * tpt));
   return it.run == 1 && ntok > 0 ? (it.ctx - it.qlen + it.tok0 + t * tpt + ntok - 1) / kKeys + 1 : 0;
 }
 
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
     } else if (warp >= kCodeWarp) {
       // ===== items, blocks, scales and codes of K (or V), ahead of the widening warps =====
       const int is_v = warp != kCodeWarp;
-      const int per_item = kTiles * tpt;
+      const int per_item = p.tiles * tpt;
       // K's warp claims the items.  Item x of the grid: kv head x % Hkv of query block x / Hkv,
       // the blocks of all sequences counted from the last one's last block down, so that a
       // sequence's long items come first; items past the last block (the grid is sized without
@@ -535,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         it.qlen = __ldg(p.query_start + it.s + 1) - it.qs;
         it.ctx = __ldg(p.context_lens + it.s);
         it.tok0 = left * per_item;
+        it.end = min(it.qlen, it.tok0 + per_item);
         if (it.ctx < 1 || it.ctx > p.max_blocks_per_seq * p.block_size || it.qlen > it.ctx) {
           it.run = 2;
           if (lane == 0) atomicOr(p.err, kErrBadContext);
@@ -573,11 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
               uint32_t tma_bytes = 0;
 #pragma unroll
               for (int t = 0; t < kTiles; ++t)
-                if (p.q_tma && it.tok0 + (t + 1) * tpt <= it.qlen) tma_bytes += kRows * D * 2;
+                if (p.q_tma && it.tok0 + (t + 1) * tpt <= it.end) tma_bytes += kRows * D * 2;
               mbar_arrive_expect_tx(smem_addr(&sm.q_full), tma_bytes);
 #pragma unroll
               for (int t = 0; t < kTiles; ++t) {
-                if (!(p.q_tma && it.tok0 + (t + 1) * tpt <= it.qlen)) continue;
+                if (!(p.q_tma && it.tok0 + (t + 1) * tpt <= it.end)) continue;
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
                   tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, it.g * G,
@@ -587,12 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             __syncwarp();
             for (int t = 0; t < kTiles; ++t) {
               const int first = it.tok0 + t * tpt;
-              if (first >= it.qlen || (p.q_tma && first + tpt <= it.qlen)) continue;
+              if (first >= it.end || (p.q_tma && first + tpt <= it.end)) continue;
               // (rows past tpt * G, where G does not divide 128, are zeros too)
               for (int u = lane; u < kRows * CH; u += 32) {
                 const int r = u / CH, c = u % CH;
                 const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
-                const bool live = tl < tpt && first + tl < it.qlen;
+                const bool live = tl < tpt && first + tl < it.end;
                 const uint8_t* src =
                     p.q + ((static_cast<size_t>(it.qs + (live ? first + tl : 0)) * p.num_q_heads +
                             it.g * G + (live ? r - tl * G : 0)) * D + c * 8) * 2;
@@ -772,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       const int n0 = key_tiles(it, 0, tpt), n1 = key_tiles(it, 1, tpt);
       const int n = max(n0, n1), ntt = t == 0 ? n0 : n1;
       const int tok = it.tok0 + t * tpt + tile_tok;
-      const int pos = tile_tok < tpt && tok < it.qlen ? it.ctx - it.qlen + tok : -1;
+      const int pos = tile_tok < tpt && tok < it.end ? it.ctx - it.qlen + tok : -1;
       const int pos_lo = it.ctx - it.qlen + it.tok0 + t * tpt;  // the tile's first position
       float m_used = -INFINITY, l_run = 0.f, vref = 0.f;
       float row_scale = p.scale_log2;  // of this row's scores, before the key tile's kref
@@ -870,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       // collide in a bank.  (clamped: a cached f16 value may have been rounded up past 65504)
       const uint32_t stage = smem_addr(sm.stage[warp]);
       const int ch = lane & 7;
-      const int toks = min(tpt, it.qlen - (it.tok0 + t * tpt));  // tokens of this query tile
+      const int toks = min(tpt, it.end - (it.tok0 + t * tpt));  // tokens of this query tile
       T* to = outp + (static_cast<size_t>(it.qs + it.tok0 + t * tpt) * p.num_q_heads + it.g * G) * D + ch * 8;
       int at[8];  // of the eight rows that this lane stores a chunk of; -1: not a row
 #pragma unroll
@@ -922,19 +926,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
 }
 
 template <int D, typename T>
-int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
+int launch(const Params& prm, int max_query_len, int sm_count, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<D>) + 1024;
   auto* kern = prefill_fp8_block_kernel<D, T>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return -3;
   cudaLaunchConfig_t cfg = {};
   // query blocks, whatever the lengths are: a part of one per sequence beyond the whole ones
-  const int per_item = kTiles * prm.tpt;
   Params q = prm;
-  q.max_blocks = (max_query_len + per_item - 1) / per_item;
-  const long long blocks = std::min(static_cast<long long>(prm.num_tokens / per_item) + prm.num_seqs,
-                                    static_cast<long long>(prm.num_seqs) * q.max_blocks);
-  if (blocks * prm.num_kv_heads > 0x7fffffffLL) return -1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks * prm.num_kv_heads));
+  auto items = [&](int tiles) -> long long {
+    const int per_item = tiles * prm.tpt;
+    q.tiles = tiles;
+    q.max_blocks = (max_query_len + per_item - 1) / per_item;
+    return std::min(static_cast<long long>(prm.num_tokens / per_item) + prm.num_seqs,
+                    static_cast<long long>(prm.num_seqs) * q.max_blocks) * prm.num_kv_heads;
+  };
+  long long count = items(kTiles);
+  // Few items: one query tile each while every item still has an SM of its own.  One prompt
+  // of 128 / 512 tokens, 8 kv heads, 4 query heads each: 8.1 / 13.0 us, 10.2 / 15.1 us with
+  // two; a chunk of 512 over 2000 cached 39.1 us, 42.5 with two.  Past that, items queue: 8
+  // chunks of 100 over 1000 cached (128 items of two) 41.0 us, 25.0 with two.
+  if (2 * count <= sm_count) count = items(1);
+  if (count > 0x7fffffffLL) return -1;
+  cfg.gridDim = dim3(static_cast<unsigned>(count));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -950,7 +963,7 @@ int launch(const Params& prm, int max_query_len, cudaStream_t stream) {
 }  // namespace prefill8
 
 int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* k_scales,
-                             const float* v_scales, cudaStream_t stream) {
+                             const float* v_scales, int sm_count, cudaStream_t stream) {
   prefill8::Params p;
   p.q = static_cast<const uint8_t*>(a.q);
   if (!kv_cache_map(&p.kmap, a.k_cache, 1, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim) ||
@@ -977,11 +990,11 @@ int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* 
   p.q_tma = q_tile_map(&p.qmap, a.q, a.num_q_heads, a.head_dim, p.group, num_tokens) ? 1 : 0;
   p.err = a.err;
   if (a.head_dim == 128)
-    return a.bf16 ? prefill8::launch<128, __nv_bfloat16>(p, a.max_query_len, stream)
-                  : prefill8::launch<128, __half>(p, a.max_query_len, stream);
+    return a.bf16 ? prefill8::launch<128, __nv_bfloat16>(p, a.max_query_len, sm_count, stream)
+                  : prefill8::launch<128, __half>(p, a.max_query_len, sm_count, stream);
   if (a.head_dim == 64)
-    return a.bf16 ? prefill8::launch<64, __nv_bfloat16>(p, a.max_query_len, stream)
-                  : prefill8::launch<64, __half>(p, a.max_query_len, stream);
+    return a.bf16 ? prefill8::launch<64, __nv_bfloat16>(p, a.max_query_len, sm_count, stream)
+                  : prefill8::launch<64, __half>(p, a.max_query_len, sm_count, stream);
   return -1;
 }
 
