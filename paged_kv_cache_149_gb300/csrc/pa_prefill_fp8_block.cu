@@ -141,7 +141,8 @@ struct Smem {
   Item item[kItems];
   unsigned long long item_full[kItems], item_free[kItems], claim_full;
   float q_factor[kTiles][kRows];       // bf16 rows of q: what turns their f16 products back
-  unsigned long long q_full, q_ready, q_free[kTiles];  // rows landed / are f16 / last S done
+  // a query tile's rows landed / are f16 / their last S is done
+  unsigned long long q_full[kTiles], q_ready[kTiles], q_free[kTiles];
   unsigned long long raw_full[2][2], raw_free[2][2];
   unsigned long long k_full[kStages], v_full[kStages];
   unsigned long long s_full[kTiles][2], p_full[kTiles][2];
@@ -342,8 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       mbar_init(smem_addr(&sm.item_free[i]), kThreads / 32 - 1);
     }
     mbar_init(smem_addr(&sm.claim_full), 1);
-    mbar_init(smem_addr(&sm.q_full), 33);  // TMA expect-tx + 32 copy lanes
-    mbar_init(smem_addr(&sm.q_ready), 2 * kWidenWarps);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_addr(&sm.raw_full[i >> 1][i & 1]), 1);
       mbar_init(smem_addr(&sm.raw_free[i >> 1][i & 1]), kWidenWarps);
@@ -354,6 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       for (int t = 0; t < kTiles; ++t) mbar_init(smem_addr(&sm.o_done[t][i]), 1);
     }
     for (int t = 0; t < kTiles; ++t) {
+      mbar_init(smem_addr(&sm.q_full[t]), 33);  // TMA expect-tx + 32 copy lanes
+      mbar_init(smem_addr(&sm.q_ready[t]), kWidenWarps);
       mbar_init(smem_addr(&sm.q_free[t]), 1);
       mbar_init(smem_addr(&sm.fin[t]), 1);
       for (int b = 0; b < 2; ++b) {
@@ -428,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         // their first tile, K's take query tile 1 after theirs.  (The softmax warps, busy writing
         // the last item out, took 7000 cycles from its last P V to the next item's first S.)
         auto q_rows = [&](int t) -> bool {
-          if (!wwait(sm.q_full, loads & 1)) return false;
+          if (!wwait(sm.q_full[t], loads & 1)) return false;
           ++loads;
           if (key_tiles(it, t, tpt) > 0)
             sm.q_factor[t][32 * cw + lane] = q_row_to_f16<D>(smem_addr(sm.q[t]), 32 * cw + lane);
           fence_async_smem();  // the rows before the tensor cores' reads
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sm.q_ready));
+          if (lane == 0) mbar_arrive(smem_addr(&sm.q_ready[t]));
           return true;
         };
         if (BF && is_v && n > 0 && !(ok = q_rows(0))) break;
@@ -568,44 +569,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         if (is_v) {
           item_done(j);
           if (it.run == 1) {
-            // ===== q: once the last item's S are done =====
+            // ===== q: each query tile once the last item's S of it are done =====
             // A whole query tile (tpt tokens x G heads = 128 rows, each token's G rows
             // contiguous in q) by TMA, one copy per 64-column half; a tile that runs past its
             // sequence by 16-byte copies, rows past the last token zeros.
-            if (loads > 0 && !(ok = wwait(sm.q_free[0], (loads - 1) & 1) && wwait(sm.q_free[1], (loads - 1) & 1)))
-              break;
-            ++loads;
-            if (lane == 0) {
-              uint32_t tma_bytes = 0;
-#pragma unroll
-              for (int t = 0; t < kTiles; ++t)
-                if (p.q_tma && it.tok0 + (t + 1) * tpt <= it.end) tma_bytes += kRows * D * 2;
-              mbar_arrive_expect_tx(smem_addr(&sm.q_full), tma_bytes);
-#pragma unroll
-              for (int t = 0; t < kTiles; ++t) {
-                if (!(p.q_tma && it.tok0 + (t + 1) * tpt <= it.end)) continue;
+            for (int t = 0; t < kTiles; ++t) {
+              if (loads > 0 && !(ok = wwait(sm.q_free[t], (loads - 1) & 1))) break;
+              const int first = it.tok0 + t * tpt;
+              const bool tma = p.q_tma && first + tpt <= it.end;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(smem_addr(&sm.q_full[t]), tma ? kRows * D * 2 : 0);
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
-                  tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, it.g * G,
-                              it.qs + it.tok0 + t * tpt, smem_addr(&sm.q_full));
+                  if (tma)
+                    tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, it.g * G,
+                                it.qs + first, smem_addr(&sm.q_full[t]));
               }
-            }
-            __syncwarp();
-            for (int t = 0; t < kTiles; ++t) {
-              const int first = it.tok0 + t * tpt;
-              if (first >= it.end || (p.q_tma && first + tpt <= it.end)) continue;
-              // (rows past tpt * G, where G does not divide 128, are zeros too)
-              for (int u = lane; u < kRows * CH; u += 32) {
-                const int r = u / CH, c = u % CH;
-                const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
-                const bool live = tl < tpt && first + tl < it.end;
-                const uint8_t* src =
-                    p.q + ((static_cast<size_t>(it.qs + (live ? first + tl : 0)) * p.num_q_heads +
-                            it.g * G + (live ? r - tl * G : 0)) * D + c * 8) * 2;
-                cp_async16(smem_addr(sm.q[t]) + swz(kRows, r, c), src, live ? 16u : 0u);
+              __syncwarp();
+              if (first < it.end && !tma) {
+                // (rows past tpt * G, where G does not divide 128, are zeros too)
+                for (int u = lane; u < kRows * CH; u += 32) {
+                  const int r = u / CH, c = u % CH;
+                  const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
+                  const bool live = tl < tpt && first + tl < it.end;
+                  const uint8_t* src =
+                      p.q + ((static_cast<size_t>(it.qs + (live ? first + tl : 0)) * p.num_q_heads +
+                              it.g * G + (live ? r - tl * G : 0)) * D + c * 8) * 2;
+                  cp_async16(smem_addr(sm.q[t]) + swz(kRows, r, c), src, live ? 16u : 0u);
+                }
               }
+              cp_async_arrive(smem_addr(&sm.q_full[t]));
             }
-            cp_async_arrive(smem_addr(&sm.q_full));
+            if (!ok) break;
+            ++loads;
           }
         }
         // Lane g < 8 looks after token group g of a tile.
@@ -732,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         const int n = __shfl_sync(0xffffffffu, max(n0, n1), 0);
         const int ntt = __shfl_sync(0xffffffffu, t == 0 ? n0 : n1, 0);
         if (n == 0) continue;
-        if (!(ok = wwait(BF ? sm.q_ready : sm.q_full, loads & 1))) break;
+        if (!(ok = wwait(BF ? sm.q_ready[t] : sm.q_full[t], loads & 1))) break;
         ++loads;
         fence_async_smem();  // q rows that lanes copied or converted -> tensor cores
         if (ntt > 0) {
@@ -740,12 +736,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           issue_s(sn, rk.st);
         }
         rk.next();
-        if (ntt <= 1) commit_el(smem_addr(&sm.q_free[t]), el);
+        // q is free once S of the last key tile is done, and the softmax has its rows' factors
+        // (by the first P, which S of the third tile waits for)
+        if (ntt == 0) commit_el(smem_addr(&sm.q_free[t]), el);
         for (int kt = 0; kt < n; ++kt, rk.next(), rv.next()) {
           if (kt + 1 < ntt) {
             if (!(ok = wwait(sm.k_full[rk.st], rk.ph))) break;
             issue_s(sn + 1, rk.st);
-            if (kt + 2 == ntt) commit_el(smem_addr(&sm.q_free[t]), el);
+            if (kt > 0 && kt + 2 == ntt) commit_el(smem_addr(&sm.q_free[t]), el);
           }
           if (!(ok = wwait(sm.v_full[rv.st], rv.ph))) break;
           if (kt < ntt) {
@@ -753,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             tc_fence_after();
             issue_pv(sn, rv.st, kt == 0);
             commit_el(smem_addr(&sm.pv_done[t][sn & 1]), el);
+            if (kt == 0 && ntt <= 2) commit_el(smem_addr(&sm.q_free[t]), el);
             ++sn;
           } else if (!(ok = wwait(sm.k_full[rv.st], rv.ph))) {
             break;
