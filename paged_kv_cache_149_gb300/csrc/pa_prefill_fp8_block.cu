@@ -31,7 +31,9 @@
 //   codes by TMA into two buffers each.
 // * Eight widening warps (four for K, four for V) turn codes into f16 in the swizzled layout
 //   that the tcgen05 descriptors read, into rings of kStages K and V tiles.  Rows past the
-//   context become zeros (what lies there is not used).
+//   context become zeros (what lies there is not used), and so do NaN codes of V from the first
+//   key tile on that some token of the item does not attend to all of: a weight of zero times
+//   NaN would reach that token.  The rows that attend to such a key get the NaN as they go out.
 // * An MMA warp per query tile: S = Q K^T into tensor memory (two buffers of 64 columns,
 //   alternate key tiles), P V from the P that the tile's softmax leaves over the first half of
 //   the S buffer, into 128 columns of O.  S of the next keys goes in before P V of the current
@@ -83,6 +85,7 @@ struct Params {
   CUtensorMap qmap;  // q as [tokens][Hq][d], box (64, G, 128 / G): one query tile's half
   int q_tma;         // qmap is valid (G divides 128)
   const uint8_t* q;
+  const uint8_t* v_cache;
   const float* k_scales;
   const float* v_scales;
   const int32_t* block_tables;
@@ -106,12 +109,39 @@ struct Item {
   int tok0, end;      // the item's tokens of the sequence
   int s;
   int bad;  // a block id of its keys is out of range
+  int nan;  // V codes of keys that not all of its tokens attend to were NaN and went in as zeros
 };
 
 // Keys that query tile t of an item needs, in tiles: up to the position of its last token.
 __device__ __forceinline__ int key_tiles(const Item& it, int t, int tpt) {
   const int ntok = min(tpt, it.end - (it.tok0 + t * tpt));
   return it.run == 1 && ntok > 0 ? (it.ctx - it.qlen + it.tok0 + t * tpt + ntok - 1) / kKeys + 1 : 0;
+}
+
+// The first key tile that not all tokens of an item attend to.
+__device__ __forceinline__ int first_masked(const Item& it) {
+  return (it.ctx - it.qlen + it.tok0 + 1) / kKeys;
+}
+
+// 0xff in the bytes of `w` that are NaN codes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
+}
+
+// NaN into the columns of one output row (D 16-bit values) in which V is NaN at a key from the
+// item's first masked tile up to the row's own position.
+template <int D>
+__device__ __forceinline__ void nan_columns(const Params& p, const Item& it, int pos, uint16_t* out) {
+  const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
+#pragma unroll 1
+  for (int key = first_masked(it) * kKeys; key <= pos; ++key) {
+    const size_t group = static_cast<size_t>(trow[key >> p.log2_block]) * p.num_kv_heads + it.g;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(
+        p.v_cache + ((group << p.log2_block) + (key & (p.block_size - 1))) * D);
+#pragma unroll 1
+    for (int i = 0; i < D; ++i)
+      if (nan_bytes(codes[i / 4]) >> (8 * (i % 4)) & 1u) out[i] = 0x7fff;
+  }
 }
 
 // A place in a ring of kStages and the parity of its current use.
@@ -459,6 +489,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
                 for (int hc = 0; hc < NH; ++hc) c[gi][hc] = make_uint4(0, 0, 0, 0);
               }
           }
+          if (is_v && kt >= first_masked(it)) {
+            // a weight of zero times NaN is NaN: such codes become zeros here, and the rows that
+            // do attend to them get their NaN in the end
+            uint32_t any = 0;
+            auto drop = [&](uint32_t& w) {
+              const uint32_t m = nan_bytes(w);
+              any |= m;
+              w &= ~m;
+            };
+#pragma unroll
+            for (int gi = 0; gi < 2; ++gi)
+#pragma unroll
+              for (int hc = 0; hc < NH; ++hc)
+                drop(c[gi][hc].x), drop(c[gi][hc].y), drop(c[gi][hc].z), drop(c[gi][hc].w);
+            if (any) sm.item[j % kItems].nan = 1;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sm.raw_free[is_v][b]));
           if (num >= kStages &&
@@ -517,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       }
       auto item_of = [&](int x) -> Item {  // (uniform over the warp)
         Item it;
-        it.run = it.bad = 0;
+        it.run = it.bad = it.nan = 0;
         const int f = total - 1 - x / p.num_kv_heads;  // query block, counted from the first
         it.g = x % p.num_kv_heads;
         if (x < 0 || f < 0) return it;
@@ -867,6 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       num += n;
       // ---- out = O vref / l (the item's tiles are done, so its bad-block flag is final) ----
       const bool good = it.run == 1 && ntt > 0 && *reinterpret_cast<volatile int*>(&sm.item[j % kItems].bad) == 0;
+      const bool nan = good && *reinterpret_cast<volatile int*>(&sm.item[j % kItems].nan) != 0;
       item_done(j);
       const float inv = vref / l_run;
       // The rows go out through shared memory, 64 columns at a time, so that each store
@@ -912,6 +959,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           if (at[i] >= 0) *reinterpret_cast<uint4*>(to + at[i] + c0) = x[i];
         __syncwarp();  // the reads before the next columns' stores
       }
+      if (nan && pos >= 0)
+        nan_columns<D>(p, it, pos,
+                       reinterpret_cast<uint16_t*>(outp) +
+                           ((static_cast<size_t>(it.qs + tok) * p.num_q_heads) + it.g * G + r - tile_tok * G) * D);
+      __syncwarp();
       // the O loads before this warp's next P, which lets the next item's P V overwrite O
       tc_fence_before();
     }
@@ -967,6 +1019,7 @@ int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* 
                              const float* v_scales, int sm_count, cudaStream_t stream) {
   prefill8::Params p;
   p.q = static_cast<const uint8_t*>(a.q);
+  p.v_cache = static_cast<const uint8_t*>(a.v_cache);
   if (!kv_cache_map(&p.kmap, a.k_cache, 1, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim) ||
       !kv_cache_map(&p.vmap, a.v_cache, 1, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim))
     return -3;

@@ -167,6 +167,31 @@ def test_a_nan_key_behind_a_token_does_not_reach_it():
     assert device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (7, 1, 64), (2, 2, 128)])
+@pytest.mark.parametrize("ctx,new,at", [(100, 100, (70,)), (500, 300, (10, 199, 200, 350, 499)), (700, 1, (699, 3)),
+                                        (64, 2, (62, 63)), (900, 900, (0, 63, 64, 640))])
+def test_a_nan_value_reaches_the_tokens_behind_it_only(dtype, hq, hkv, d, ctx, new, at):
+    """NaN in a value's column: NaN in that column for its head's queries from its token on, and
+    every other output as it is with a zero there."""
+    b = Batch([ctx, 40], hq, hkv, d, 16, dtype, seed=7)
+    k8, v8, ks, vs = b.written()
+    qs = np.array([0, new, new + 40], np.int32)
+    q = dev16(rows16(b.rng, (new + 40, hq, d), dtype), dtype)
+    run = lambda v: pa.prefill_fp8_block(q, dev(k8), dev(v), dev(ks), dev(vs), dev(b.tables), dev(b.ctx), dev(qs), 0.1, max(new, 40))  # noqa: E731
+    vz, vn, G = v8.copy(), v8.copy(), hq // hkv
+    nan = np.zeros((new + 40, hq, d), bool)
+    for i, t in enumerate(at):
+        h, c = i % hkv, (5 + 13 * i) % d
+        vz[b.tables[0, t // 16], h, t % 16, c] = 0
+        vn[b.tables[0, t // 16], h, t % 16, c] = 0x7F if i % 2 else 0xFF
+        nan[max(0, t - (ctx - new)):new, h * G:(h + 1) * G, c] = True
+    want, got = run(vz), run(vn)
+    nan = torch.from_numpy(nan).cuda()
+    assert torch.isnan(got[nan]).all() and torch.equal(got[~nan], want[~nan])
+    assert torch.isfinite(want).all() and device_error() == 0
+
+
 # --------------------------------------------------------------------------------- large caches
 
 def test_caches_past_4_gib():
