@@ -44,6 +44,13 @@
 //   only gain from it; the final O / l uses the same m.  (A limit of 8: 285 us, 15: 270 us for
 //   8 prompts of 2048 tokens whose blocks' scales spread over 2^4.)
 // Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag.
+//
+// What bounds it: the softmax's step of 64 keys, about 1710 cycles against 1024 of tensor work,
+// at 1240 instructions a step on each of an SM's schedulers (mostly exponentials, maxima, sums
+// and the widening); then 5300 to 9000 cycles from an item's last P to the next item's first.
+// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 269 us (1020
+// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 196 us (950 TFLOP/s).  The 16-bit
+// prefill takes 292 and 202 us there.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

