@@ -265,23 +265,33 @@ struct Stage {
 
 struct StageIt {
   Fam f;
-  int kvh, j, jb;
+  int kvh, j, jb, step;
 };
 
-__device__ __forceinline__ void stage_it_enter(StageIt& it, int pi, int phase, long long w0,
-                                               long long w1, const Params& p) {
+// Which of a pair's P warps has a family of at most `narrow` units to itself (FB, P > 1; see
+// the kernel's set-up).  They take such families in turn.
+__device__ __forceinline__ int narrow_owner(const Fam& f, const Params& p) {
+  return (f.s * p.ngroups + f.g) & (p.phases - 1);
+}
+__device__ __forceinline__ bool takes_part(const Fam& f, int phase, int narrow, const Params& p) {
+  return f.ns > narrow || narrow_owner(f, p) == phase;
+}
+
+__device__ __forceinline__ void stage_it_enter(StageIt& it, int pi, int phase, int narrow,
+                                               long long w0, long long w1, const Params& p) {
   const int2 r = unit_range(it.f, pi, w0, w1, p);
-  if (!fam_valid(it.f) || r.x >= r.y) {
+  if (!fam_valid(it.f) || r.x >= r.y || !takes_part(it.f, phase, narrow, p)) {
     it.j = it.jb = 0;
     return;
   }
   it.kvh = pair_heads(p, it.f.g * p.gs + pi).kvh;
-  it.j = r.x + (phase - r.x % p.phases + p.phases) % p.phases;
+  it.step = it.f.ns > narrow ? p.phases : 1;
+  it.j = it.f.ns > narrow ? r.x + (phase - r.x % p.phases + p.phases) % p.phases : r.x;
   it.jb = r.y;
 }
 
-__device__ __forceinline__ bool next_stage(StageIt& it, int pi, int phase, long long w0, long long w1,
-                                           Stage& st, const Params& p) {
+__device__ __forceinline__ bool next_stage(StageIt& it, int pi, int phase, int narrow, long long w0,
+                                           long long w1, Stage& st, const Params& p) {
   for (;;) {
     if (it.j < it.jb) {
       st.s = it.f.s;
@@ -289,12 +299,12 @@ __device__ __forceinline__ bool next_stage(StageIt& it, int pi, int phase, long 
       st.t0 = it.j << p.log2_stage;
       st.nt = min(1 << p.log2_stage, it.f.ctx - st.t0);
       st.last = st.t0 + st.nt == it.f.ctx;
-      it.j += p.phases;
+      it.j += it.step;
       return true;
     }
     fam_next(it.f, p);
     if (it.f.s >= p.num_seqs || it.f.pre >= w1) return false;
-    stage_it_enter(it, pi, phase, w0, w1, p);
+    stage_it_enter(it, pi, phase, narrow, w0, w1, p);
   }
 }
 
@@ -1035,13 +1045,13 @@ __device__ __forceinline__ void load_q4(const Params& p, int s, int h0, int nh, 
 }
 
 // The next family (after f) where pair pi has units to compute; false at the share's end.
-__device__ __forceinline__ bool next_busy_fam(Fam f, int pi, long long w0, long long w1,
-                                              const Params& p, Fam& out) {
+__device__ __forceinline__ bool next_busy_fam(Fam f, int pi, int phase, int narrow, long long w0,
+                                              long long w1, const Params& p, Fam& out) {
   for (;;) {
     fam_next(f, p);
     if (f.s >= p.num_seqs || f.pre >= w1) return false;
     const int2 r = unit_range(f, pi, w0, w1, p);
-    if (fam_valid(f) && r.x < r.y) {
+    if (fam_valid(f) && r.x < r.y && takes_part(f, phase, narrow, p)) {
       out = f;
       return true;
     }
@@ -1155,6 +1165,19 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     G = static_cast<int>(min(static_cast<long long>(G), max(1ll, W / share)));
     if (c >= G) return;  // (uniform over the CTA)
   }
+  // FB: the warps of a pair do not share a family of at most `narrow` units, they take such in
+  // turn.  Sharing costs barriers and an exchange of O, about as much as three units computed
+  // one after the other; a warp alone leaves the others to the share's other families, so the
+  // more families a share has the longer they may be.  142 sequences of up to 8 tokens, 3 kv
+  // heads of 128, 16 query heads each: 26.7 -> 9.8 us; 212 of up to 153: 46.3 -> 21.4; 125 of up
+  // to 622 (64-wide heads) 20.0 with any limit up to 3 units a family of the share, 22.9 with 6.
+  int narrow = 0;
+  if constexpr (FB) {
+    if (P > 1) {
+      const long long families = static_cast<long long>(p.num_seqs) * p.ngroups;
+      narrow = 3 * static_cast<int>(min(static_cast<long long>(P), max(1ll, families / G)));
+    }
+  }
   long long w0, w1;
   share_of(c, W, G, w0, w1);
   if (w0 < w1 && excl <= w0 && w0 < excl + mine) {
@@ -1189,10 +1212,10 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   const int rsub = lane / G_::kRowChunks;  // and its first row
   StageIt sit;
   sit.f = first;
-  stage_it_enter(sit, pi, phase, w0, w1, p);
+  stage_it_enter(sit, pi, phase, narrow, w0, w1, p);
   constexpr int NE = G_::kMaxSpan;
   Stage nxt;
-  bool nxt_ok = next_stage(sit, pi, phase, w0, w1, nxt, p);
+  bool nxt_ok = next_stage(sit, pi, phase, narrow, w0, w1, nxt, p);
   int nxt_e[NE];
 #pragma unroll
   for (int k = 0; k < NE; ++k) nxt_e[k] = 0;
@@ -1314,7 +1337,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
         }
       }
       ++issued;
-      nxt_ok = next_stage(sit, pi, phase, w0, w1, nxt, p);
+      nxt_ok = next_stage(sit, pi, phase, narrow, w0, w1, nxt, p);
       if (nxt_ok) stage_entries<NE>(nxt, p, nxt_e);
     }
     cp_async_commit();  // one group per call, empty or not
@@ -1367,9 +1390,9 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   {
     const int2 r = unit_range(first, pi, w0, w1, p);
     Fam qf;
-    bool have = fam_valid(first) && r.x < r.y;
+    bool have = fam_valid(first) && r.x < r.y && takes_part(first, phase, narrow, p);
     if (have) qf = first;
-    else have = next_busy_fam(first, pi, w0, w1, p, qf);
+    else have = next_busy_fam(first, pi, phase, narrow, w0, w1, p, qf);
     if (have) {
       const PairHeads ph = pair_heads(p, qf.g * p.gs + pi);
       if (I4) load_q4<D, NTH, T>(p, qf.s, ph.h0, ph.nh, lane, qn);
@@ -1399,6 +1422,14 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       }
       continue;
     }
+    const bool alone = f.ns <= narrow;
+    if (alone && narrow_owner(f, p) != phase) {  // another warp's: only its piece is noted here
+      if (r.x > 0 || r.y < f.ns) {
+        (ncut == 0 ? cut_a : cut_b) = cut_piece(f, pi, ph, W, G, p);
+        ++ncut;
+      }
+      continue;
+    }
     const bool computes = r.x < r.y;  // (an empty middle piece computes nothing)
     uint32_t qb[KS][NTH][2];
     if (computes) {
@@ -1410,7 +1441,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           qb[ks][nt][1] = qn[ks][nt][1];
         }
       Fam qf;
-      if (next_busy_fam(f, pi, w0, w1, p, qf)) {
+      if (next_busy_fam(f, pi, phase, narrow, w0, w1, p, qf)) {
         const PairHeads lh = pair_heads(p, qf.g * p.gs + pi);
         if (I4) load_q4<D, NTH, T>(p, qf.s, lh.h0, lh.nh, lane, qn);
         else if (F8) load_q8<D, NTH, T>(p, qf.s, lh.h0, lh.nh, lane, qn);
@@ -1458,8 +1489,8 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     // FB: the largest V scale met so far (O holds sums over it), and its reciprocal
     float v_ref = 0.f, v_inv = 0.f;
 
-    const int j_first = r.x + (phase - r.x % P + P) % P;
-    for (int j = j_first; j < r.y; j += P) {
+    const int j_first = alone ? r.x : r.x + (phase - r.x % P + P) % P;
+    for (int j = j_first; j < r.y; j += alone ? 1 : P) {
       issue_one();                   // stage used + kAhead goes in flight
       const uint32_t slot = used % R;
       ++used;
@@ -1885,7 +1916,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     float* pacc = p.part_acc + piece * p.heads_per_pair * D;
     float* pml = p.part_ml + piece * p.heads_per_pair * 2;
 
-    if (P == 1) {
+    if (P == 1 || alone) {
       // ---------- pair end, one warp per pair: everything stays in registers ----------
       // Lane (r0, qc) holds O^T rows d = 16*mt + r0 (+8) for heads h = 8*nt + qc (+1), and
       // the running max/sum of those heads.
@@ -1912,7 +1943,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           }
         CutPiece& cpr = ncut == 0 ? cut_a : cut_b;
         cpr = cut_piece(f, pi, ph, W, G, p);
-        if (f.pre + f.fw < w1) {
+        if (P == 1 && f.pre + f.fw < w1) {
           // More of the share follows (this is its first family, or a middle one): count
           // the piece in now, so that the share's end has one arrival and merge fewer.
           // The pair's other pieces lie in earlier shares, so this arrival rarely

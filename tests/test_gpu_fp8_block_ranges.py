@@ -129,6 +129,30 @@ def test_decode_of_few_long_sequences(hq, hkv, d, ctx):
     check_rows(b, caches, got, q, np.arange(len(ctx) + 1), scale, lambda n: range(n))
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(7, 1, 64), (48, 3, 128), (10, 5, 64), (12, 12, 128), (4, 2, 128)])
+@pytest.mark.parametrize("n", [3, 40, 330])
+def test_decode_of_short_sequences_with_few_or_odd_heads(hq, hkv, d, n):
+    """Sequences that one warp takes among others that several share, contexts that are invalid
+    and a block outside the pool among them."""
+    ctx = [1 + (29 * i) % 70 if i % 5 else 1 + (311 * i) % 900 for i in range(n)]
+    b = Batch(ctx, hq, hkv, d, 8, "bf16", seed=n)
+    caches = b.written()
+    q_bits = rows16(b.rng, (n, hq, d), "bf16")
+    q, scale = decode_bits(q_bits, "bf16"), 1.0 / np.sqrt(d)
+    tables, lens = b.tables.copy(), b.ctx.copy()
+    zeros = [1] if n == 3 else [1, 7, n // 2, n - 1]
+    lens[zeros[0]] = 0
+    for s in zeros[1:]:
+        tables[s, (lens[s] - 1) // 8] = -1 if s % 2 else b.nb
+    out = pa.decode_fp8_block(dev16(q_bits, "bf16"), *upload(caches), dev(tables), dev(lens), scale)
+    got = values(out, "bf16")
+    assert device_error() == pa.DEVERR_BAD_CONTEXT | (pa.DEVERR_BAD_BLOCK if n > 3 else 0)
+    assert (got[zeros] == 0).all()
+    keep = np.setdiff1d(np.arange(n), zeros)
+    b.ctx, b.tables = b.ctx[keep], b.tables[keep]
+    check_rows(b, caches, got[keep], q[keep], np.arange(len(keep) + 1), scale, lambda m: range(m))
+
+
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (8, 8), (4, 1)])
 @pytest.mark.parametrize("ctx", [40, 4000])
 def test_a_nan_code_reaches_its_head_and_no_other(hq, hkv, ctx):
