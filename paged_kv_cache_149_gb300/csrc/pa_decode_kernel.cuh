@@ -189,14 +189,15 @@ struct Fam {
   int s, g, ctx, ns;
   bool ok;        // 1 <= ctx <= max_ctx
   long long pre;  // first stage unit of the family
-  long long fw;   // its weight: ns * gs + seg_cost
+  long long fw;   // its weight: ns * gs + seg_cost, at least fw_min (FB; else 0)
+  int fw_min;
 };
 
 __device__ __forceinline__ void fam_load(Fam& f, const Params& p) {
   f.ctx = __ldg(p.context_lens + f.s);
   f.ok = f.ctx >= 1 && f.ctx <= p.max_ctx;
   f.ns = pair_stages(f.ctx, p);
-  f.fw = static_cast<long long>(f.ns) * p.gs + p.seg_cost;
+  f.fw = max(static_cast<long long>(f.ns) * p.gs + p.seg_cost, static_cast<long long>(f.fw_min));
 }
 
 __device__ __forceinline__ void fam_next(Fam& f, const Params& p) {
@@ -1149,6 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   const long long excl = before + incl - mine;
   int G = gridDim.x;
   const int c = blockIdx.x;
+  int fw_min = 0;
   if constexpr (FB) {
     // Few shares for few long sequences.  A sequence of n steps (a step: one stage for each
     // of the eight warps) in shares of R steps takes about R step times and then the merge of
@@ -1160,9 +1162,22 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     // any); 8 sequences of 8-32 K tokens are cut as before.
     int longest = 0;
     for (int w = 0; w < kWarps; ++w) longest = max(longest, sm.longest[w]);
-    const float steps = sqrtf(static_cast<float>(longest) * p.piece_cost);
-    const long long share = kWarps * static_cast<long long>(fmaxf(steps, 1.f));
-    G = static_cast<int>(min(static_cast<long long>(G), max(1ll, W / share)));
+    const long long families = static_cast<long long>(p.num_seqs) * p.ngroups;
+    if (families <= G && longest <= (4 + p.heads_per_pair / 2) * p.phases) {
+      // Few short sequences: every family whole, on a CTA of its own (equal weights make equal
+      // shares).  Counting pieces in and merging them takes as long as about 4 steps, and more
+      // with more heads.  4 sequences of up to 64 / 128 / 192 tokens, 8 kv heads of 128, 4 query
+      // heads each: 6.1 / 8.9 / 11.2 us against 11.2 / 11.4 / 11.8 cut, 256 (8 steps) 13.8
+      // against 12.3; 16 query heads each, 192 / 320 / 512: 19.0 / 25.1 / 35.9 against 31.5 /
+      // 33.2 / 38.4.
+      fw_min = longest * p.gs + p.seg_cost;
+      G = static_cast<int>(families);
+      W = families * fw_min;
+    } else {
+      const float steps = sqrtf(static_cast<float>(longest) * p.piece_cost);
+      const long long share = kWarps * static_cast<long long>(fmaxf(steps, 1.f));
+      G = static_cast<int>(min(static_cast<long long>(G), max(1ll, W / share)));
+    }
     if (c >= G) return;  // (uniform over the CTA)
   }
   // FB: the warps of a pair do not share a family of at most `narrow` units, they take such in
@@ -1180,7 +1195,12 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   }
   long long w0, w1;
   share_of(c, W, G, w0, w1);
-  if (w0 < w1 && excl <= w0 && w0 < excl + mine) {
+  if (fw_min > 0) {
+    if (tid == 0) {
+      sm.start_s = c / p.ngroups;
+      sm.start_pre = static_cast<long long>(sm.start_s) * p.ngroups * fw_min;
+    }
+  } else if (w0 < w1 && excl <= w0 && w0 < excl + mine) {
     long long pre = excl;
     int s = sa;
     for (;; ++s) {
@@ -1200,6 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   first.s = sm.start_s;
   first.g = 0;
   first.pre = sm.start_pre;
+  first.fw_min = fw_min;
   fam_load(first, p);
   while (w0 >= first.pre + first.fw) {  // the family holding unit w0
     first.pre += first.fw;
