@@ -293,7 +293,8 @@ int pa_build_step(const int32_t* query_lens, const int32_t* context_lens, int nu
  *   earlier rows of the block, where S > scales[b][h]: code := E4M3(decode(code) *
  *   scales[b][h] / S) (for powers of two exact, but where the result is subnormal);
  *   new rows: code = E4M3(x / S), rounding to nearest-even, magnitudes above 448 S (only
- *   infinities) clamped, NaN kept.  scales[b][h] = S.
+ *   infinities) clamped, NaN kept.  scales[b][h] = S.  (Where an earlier scale that is no
+ *   power of two stays, x is multiplied by its rounded reciprocal.)
  * Rows of a touched block behind the last new one are left as they were.  A touched block
  * must belong to one sequence of the call (copy-on-write first), and its rows before c - q
  * must have been written by this call's kind.  A sequence with an impossible span
@@ -327,8 +328,9 @@ int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
  * or written for it; rows behind the last sequence are not touched), and scale > 0.
  * Products run in f16: codes are widened relative to the largest scale near them, bf16 rows
  * of q brought to the type's upper range by a power of two, softmax weights rounded to f16;
- * accumulation fp32; outputs clamped as by pa_decode_fp8_block.  Write the sequences' new
- * tokens first (pa_append_fp8_block). */
+ * accumulation fp32; outputs clamped as by pa_decode_fp8_block.  A NaN code reaches the tokens
+ * that attend to it and no others.  Write the sequences' new tokens first
+ * (pa_append_fp8_block). */
 int pa_prefill_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                          const float* k_scales, const float* v_scales,
                          const int32_t* block_tables, int max_blocks_per_seq,

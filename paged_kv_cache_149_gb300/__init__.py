@@ -752,6 +752,15 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _empty_like(t, stream):
+    """A new tensor like `t`, allocated for the stream that the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _block_scaled(k_cache, v_cache, k_scales, v_scales, d):
     """(num_blocks, num_kv_heads, block_size) of the caches, checked against each other."""
     nb, hkv, bs, d2 = shape = k_cache.shape
@@ -849,7 +858,7 @@ def decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, cont
     _need(tn == n, "block_tables must be [num_seqs, T]")
     _need(context_lens.shape == (n,), "context_lens must be [num_seqs]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     elif out.shape != shape or out.dtype is not dt:
         raise ValueError("out must match q")
     if workspace is None:
@@ -885,7 +894,7 @@ def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, con
     _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
     _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     elif out.shape != shape or out.dtype is not dt:
         raise ValueError("out must match q")
     args = (_ptr(q, "q", dt, dev), _codes_ptr(k_cache, "k_cache", dev),

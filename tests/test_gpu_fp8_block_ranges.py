@@ -77,6 +77,16 @@ def test_more_sequences_than_lanes_keep_apart():
     check_rows(b, caches, got, q, qs, 0.125, lambda n: range(n))
 
 
+@pytest.mark.parametrize("hq,hkv", [(64, 1), (33, 1), (96, 2), (65, 5)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_of_wide_and_odd_groups(hq, hkv, d):
+    b = Batch([70, 9, 200], hq, hkv, d, 16, "bf16", seed=hq)
+    caches = b.written()
+    got, q, qs = prefill(b, caches, [70, 4, 30])
+    assert device_error() == 0
+    check_rows(b, caches, got, q, qs, 1.0 / np.sqrt(d), lambda n: (0, n // 2, n - 1))
+
+
 def test_spans_past_max_query_len_and_past_the_rows():
     """Rows past max_query_len's query blocks are not computed; a span that is not the call's
     touches nothing and is reported."""
@@ -342,6 +352,27 @@ def test_steps_on_two_streams_at_once():
     for st, want in zip(sts, alone):
         for a, c in zip(_results(st, st["used"]), want):
             assert torch.equal(a, c)
+
+
+def test_outputs_are_allocated_for_the_stream_of_the_call():
+    """The memory of a tensor freed on the current stream, with work on it still under way there,
+    is not handed to a call on another stream."""
+    b = Batch([130, 64, 7, 300], 8, 2, 128, 16, "bf16", seed=10)
+    st = _step(b, 8, 24)
+    st["pair"] = dev([[0, b.nb - 1]], np.int32)
+    _run(st, 16, b.nb, 300)
+    torch.cuda.synchronize()
+    side, args = torch.cuda.Stream(), (*st["caches"], st["tables"], st["lens"])
+    for _ in range(10):
+        junk = torch.empty_like(st["out"])
+        for _ in range(50):
+            junk.fill_(9)
+        del junk
+        out = pa.prefill_fp8_block(st["q"], *args, st["qs"], 0.1, 300, stream=side)
+        one = pa.decode_fp8_block(st["q"][:4], *args, 0.1, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, st["out"]) and torch.equal(one, st["one"])
+    assert device_error() == 0
 
 
 def test_planned_calls_run_again_on_any_stream():
