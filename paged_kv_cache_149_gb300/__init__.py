@@ -699,7 +699,31 @@ def swap_blocks_int4(src, dst, block_mapping, stream=None, device=None):
 
 # ---- FP8 blocks with a scale per (block, kv head), and the step's bookkeeping ----
 # A serving step makes these calls back to back, several of them shorter on the GPU than in
-# Python, so their checks touch each tensor as little as possible.
+# Python, so their checks touch each tensor as little as possible, and what they need of torch
+# is looked up once.
+
+class _Torch:
+    """What the calls below need of torch (their first call imports it)."""
+
+    def __init__(self):
+        import torch
+        self.i32, self.i64, self.f32, self.u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+        self.f8, self.f16, self.bf16 = torch.float8_e4m3fn, torch.float16, torch.bfloat16
+        self.module, self.empty_like, self.device = torch, torch.empty_like, torch.cuda.device
+        # (None in a torch without CUDA, whose tensors no call gets as far with)
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+_T = None
+
+
+def _torch():
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
+
 
 def _ptr(t, name, dtype, dev):
     """Address of a contiguous tensor of `dtype` on CUDA device number `dev`."""
@@ -710,10 +734,20 @@ def _ptr(t, name, dtype, dev):
 
 def _codes_ptr(t, name, dev):
     """The same of E4M3 codes (uint8 or float8_e4m3fn)."""
-    import torch
-    if (t.dtype is torch.uint8 or t.dtype is torch.float8_e4m3fn) and t.get_device() == dev and t.is_contiguous():
+    T = _T or _torch()
+    dt = t.dtype
+    if (dt is T.u8 or dt is T.f8) and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    return _refuse(t, name, (torch.uint8, torch.float8_e4m3fn), dev)
+    return _refuse(t, name, (T.u8, T.f8), dev)
+
+
+def _code16(dtype):
+    T = _T or _torch()
+    if dtype is T.bf16:
+        return PA_BF16
+    if dtype is T.f16:
+        return PA_FP16
+    raise TypeError(f"unsupported dtype {dtype}; expected float16 or bfloat16")
 
 
 def _device_of(t, name):
@@ -735,30 +769,26 @@ def _on_its_device(fn):
     """Decorator: run the call with the device of its first tensor current."""
     @functools.wraps(fn)
     def wrapped(t, *args, **kw):
-        import torch
-        first = t[0] if isinstance(t, (tuple, list)) else t
-        dev = first.get_device()
-        if dev < 0 or dev == torch._C._cuda_getDevice():
+        T = _T or _torch()
+        dev = t.get_device()
+        if dev < 0 or dev == T.current_device():
             return fn(t, *args, **kw)
-        with torch.cuda.device(dev):
+        with T.device(dev):
             return fn(t, *args, **kw)
     return wrapped
 
 
 def _raw_stream(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return (_T or _torch()).raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _empty_like(t, stream):
     """A new tensor like `t`, allocated for the stream that the call runs on."""
-    import torch
+    T = _T or _torch()
     if stream is None:
-        return torch.empty_like(t)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t)
+        return T.empty_like(t)
+    with T.module.cuda.stream(stream):
+        return T.empty_like(t)
 
 
 def _block_scaled(k_cache, v_cache, k_scales, v_scales, d):
@@ -780,8 +810,8 @@ def build_step(query_lens, context_lens, free_blocks, free_start, block_tables, 
     (query_start [num_seqs + 1], free_next [1]).  A step that lacks blocks or slots changes
     no table, sets every slot to -1 and a device error bit.  plan=True returns a Launch whose
     runs return query_start (query_start and free_next must then be given)."""
-    import torch
-    dev, i32 = _device_of(query_lens, "query_lens"), torch.int32
+    T = _T or _torch()
+    torch, dev, i32 = T.module, _device_of(query_lens, "query_lens"), T.i32
     n, = query_lens.shape
     tn, width = block_tables.shape
     _need(context_lens.shape == (n,), "query_lens and context_lens must be [num_seqs]")
@@ -801,7 +831,7 @@ def build_step(query_lens, context_lens, free_blocks, free_start, block_tables, 
     args = (_ptr(query_lens, "query_lens", i32, dev), _ptr(context_lens, "context_lens", i32, dev),
             n, _ptr(free_blocks, "free_blocks", i32, dev), nfree,
             _ptr(free_start, "free_start", i32, dev), _ptr(block_tables, "block_tables", i32, dev),
-            width, int(block_size), int(num_blocks), _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
+            width, int(block_size), int(num_blocks), _ptr(slot_mapping, "slot_mapping", T.i64, dev),
             slots, _ptr(query_start, "query_start", i32, dev), _ptr(free_next, "free_next", i32, dev))
     if plan:
         return Launch("pa_build_step", args, query_start,
@@ -821,8 +851,8 @@ def append_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tab
     q_len .. context_lens[s] - 1.  A block's scale is the smallest power of two that holds
     its rows; where a new row raises it, the block's earlier rows are requantised.  Rows
     behind the last sequence are not read.  plan=True returns a Launch instead of writing."""
-    import torch
-    dev, i32, dt, f32 = _device_of(key, "key"), torch.int32, key.dtype, torch.float32
+    T = _T or _torch()
+    dev, i32, dt, f32 = _device_of(key, "key"), T.i32, key.dtype, T.f32
     ntok, heads, d = shape = key.shape
     n, width = block_tables.shape
     nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
@@ -834,7 +864,7 @@ def append_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tab
             _ptr(k_scales, "k_scales", f32, dev), _ptr(v_scales, "v_scales", f32, dev),
             _ptr(block_tables, "block_tables", i32, dev), width,
             _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
-            n, ntok, nb, hkv, d, bs, _dtype_code(key))
+            n, ntok, nb, hkv, d, bs, _code16(dt))
     if plan:
         return Launch("pa_append_fp8_block", args, k_cache,
                       keep=(key, value, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -850,8 +880,8 @@ def decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, cont
     """Paged decode over FP8 blocks with a scale per (block, kv head) (codes [NB, Hkv, B, d],
     scales [NB, Hkv] float32); q and out are fp16 or bf16.  plan=True returns a Launch
     instead of launching."""
-    import torch
-    dev, i32, dt, f32 = _device_of(q, "q"), torch.int32, q.dtype, torch.float32
+    T = _T or _torch()
+    dev, i32, dt, f32 = _device_of(q, "q"), T.i32, q.dtype, T.f32
     n, hq, d = shape = q.shape
     tn, width = block_tables.shape
     nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
@@ -868,7 +898,7 @@ def decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, cont
             _ptr(v_scales, "v_scales", f32, dev), _ptr(block_tables, "block_tables", i32, dev),
             width, _ptr(context_lens, "context_lens", i32, dev), n, hq, hkv, d, bs, nb, float(scale),
             _ptr(out, "out", dt, dev), _ptr(workspace, "workspace", workspace.dtype, dev),
-            workspace.numel() * workspace.element_size(), _dtype_code(q))
+            workspace.numel() * workspace.element_size(), _code16(dt))
     if plan:
         return Launch("pa_decode_fp8_block", args, out,
                       keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -886,8 +916,8 @@ def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, con
     sequence's newest tokens over its paged context; the tokens' own rows must already be in
     the cache (append_fp8_block).  scale must be positive.  plan=True returns a Launch
     instead of launching."""
-    import torch
-    dev, i32, dt, f32 = _device_of(q, "q"), torch.int32, q.dtype, torch.float32
+    T = _T or _torch()
+    dev, i32, dt, f32 = _device_of(q, "q"), T.i32, q.dtype, T.f32
     ntok, hq, d = shape = q.shape
     n, width = block_tables.shape
     nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
@@ -902,7 +932,7 @@ def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, con
             _ptr(v_scales, "v_scales", f32, dev), _ptr(block_tables, "block_tables", i32, dev),
             width, _ptr(context_lens, "context_lens", i32, dev),
             _ptr(query_start, "query_start", i32, dev), n, ntok, int(max_query_len), hq, hkv, d, bs, nb,
-            float(scale), _ptr(out, "out", dt, dev), _dtype_code(q))
+            float(scale), _ptr(out, "out", dt, dev), _code16(dt))
     if plan:
         return Launch("pa_prefill_fp8_block", args, out,
                       keep=(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -917,8 +947,8 @@ def prefill_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, con
 def copy_blocks_fp8_block(k_cache, v_cache, k_scales, v_scales, block_mapping, stream=None):
     """copy_blocks for FP8 blocks with block scales: codes and scales of each (src, dst) pair
     in one launch."""
-    import torch
-    dev, f32 = _device_of(k_cache, "k_cache"), torch.float32
+    T = _T or _torch()
+    dev, f32 = _device_of(k_cache, "k_cache"), T.f32
     d = k_cache.shape[3]
     nb, hkv, bs = _block_scaled(k_cache, v_cache, k_scales, v_scales, d)
     pairs, two = block_mapping.shape
@@ -926,7 +956,7 @@ def copy_blocks_fp8_block(k_cache, v_cache, k_scales, v_scales, block_mapping, s
     st = lib().pa_copy_blocks_fp8_block(
         _codes_ptr(k_cache, "k_cache", dev), _codes_ptr(v_cache, "v_cache", dev),
         _ptr(k_scales, "k_scales", f32, dev), _ptr(v_scales, "v_scales", f32, dev),
-        _ptr(block_mapping, "block_mapping", torch.int32, dev), pairs, nb, hkv, d, bs,
+        _ptr(block_mapping, "block_mapping", T.i32, dev), pairs, nb, hkv, d, bs,
         _raw_stream(stream, dev))
     if st < 0:
         _check(st, "pa_copy_blocks_fp8_block")
