@@ -1176,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     } else {
       const float steps = sqrtf(static_cast<float>(longest) * p.piece_cost);
       const long long share = kWarps * static_cast<long long>(fmaxf(steps, 1.f));
-      G = static_cast<int>(min(static_cast<long long>(G), max(1ll, W / share)));
+      if (W < share * G) G = static_cast<int>(max(1ll, W / share));
     }
     if (c >= G) return;  // (uniform over the CTA)
   }
@@ -1190,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   if constexpr (FB) {
     if (P > 1) {
       const long long families = static_cast<long long>(p.num_seqs) * p.ngroups;
-      narrow = 3 * static_cast<int>(min(static_cast<long long>(P), max(1ll, families / G)));
+      narrow = 3 * max(1, static_cast<int>(min(families, static_cast<long long>(P) * G)) / G);
     }
   }
   long long w0, w1;
