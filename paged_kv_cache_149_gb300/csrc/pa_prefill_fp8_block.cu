@@ -5,14 +5,13 @@
 // With K_t = sK_t code(K_t), V_t likewise (s: the scale of token t's block and head), the token
 // at position p attends to positions t <= p:
 //   out = sum_t softmax_t(scale <q, K_t>) V_t
-// (daiw.org "Paged Attention", section 回顾与衔接; chenyuan1125 "vllm-pagedattention", section
-// 它和 FlashAttention…).
+// (daiw.org "Paged Attention", section 回顾与衔接).
 //
 // Everything runs on the tensor cores in f16, whatever q's type: a code times a power of two
 // is exact there, the widening from E4M3 is one instruction for two values, and P keeps 11
 // bits.  Range is kept by references: a key tile's codes are widened to code * s / kref, kref
 // the tile's largest K scale, and its scores multiplied by kref where the softmax scales them
-// anyway; V's to code * s / vref, vref the largest V scale of the CTA's first tile (it moves,
+// anyway; V's to code * s / vref, vref the largest V scale of the item's first tile (it moves,
 // with one rescale of O, only when a later scale is over 2^7 times it); each bf16 row of q
 // is multiplied by the power of two that brings its largest value to [2^14, 2^15).  For scales
 // that are powers of two no step rounds but those of values 2^-15 and more below their
