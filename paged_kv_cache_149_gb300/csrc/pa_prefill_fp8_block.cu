@@ -26,8 +26,8 @@
 // items makes them one query tile each (see the launch).
 // * A query tile's rows are (token, query head of the kv head) pairs, 128 / G tokens x G
 //   heads; both tiles of the CTA share the key tiles (64 keys each).
-// * Two producer warps (K, V) look blocks and scales up a tile ahead and copy whole blocks of
-//   codes by TMA into two buffers each.
+// * Two producer warps (K, V) look blocks and scales up four tiles at once, four ahead, and copy
+//   whole blocks of codes by TMA into two buffers each.
 // * Eight widening warps (four for K, four for V) turn codes into f16 in the swizzled layout
 //   that the tcgen05 descriptors read, into rings of kStages K and V tiles.  Rows past the
 //   context become zeros (what lies there is not used), and so do NaN codes of V from the first
@@ -47,8 +47,8 @@
 // What bounds it: the softmax's step of 64 keys, about 1710 cycles against 1024 of tensor work,
 // at 1240 instructions a step on each of an SM's schedulers (mostly exponentials, maxima, sums
 // and the widening); then 5300 to 9000 cycles from an item's last P to the next item's first.
-// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 269 us (1020
-// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 196 us (950 TFLOP/s).  The 16-bit
+// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 267 us (1030
+// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 188 us (995 TFLOP/s).  The 16-bit
 // prefill takes 292 and 202 us there.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -600,7 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         }
         return it;
       };
-      const bool first_group = ((8 * lane) & (p.block_size - 1)) == 0;  // of its block
+      // Four key tiles are looked up at once: lane 8 q + g looks after token group g of tile q of
+      // the four.  (One tile at a time took this warp about 1650 cycles each, as long as the
+      // softmax's step.)
+      const int grp = lane & 7, quad = lane >> 3;
+      const bool first_group = ((8 * grp) & (p.block_size - 1)) == 0;  // of its block
+      auto max8 = [&](float x) -> float {  // over the lanes of a tile; scales are positive
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        return x;
+      };
       uint32_t num = 0, claims = 0, loads = 0;  // key tiles, claims and q loads so far
       Item it;
       if (!is_v) it = item_of(blockIdx.x);
@@ -656,14 +665,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             ++loads;
           }
         }
-        // Lane g < 8 looks after token group g of a tile.
         const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
         // does tile kt's group hold keys that are used
-        auto used = [&](int kt) -> bool { return lane < kGroups && kt < n && kt * kKeys + 8 * lane < it.ctx; };
-        // its table entry; checked a tile later, when it is used, so that nothing waits for the
+        auto used = [&](int kt) -> bool { return kt < n && kt * kKeys + 8 * grp < it.ctx; };
+        // its table entry; checked four tiles later, when it is used, so that nothing waits for the
         // load (the loads here are volatile to stay where they are written)
         auto entry = [&](int kt) -> int {
-          return used(kt) ? static_cast<int>(ld_early(trow + ((kt * kKeys + 8 * lane) >> p.log2_block))) : -1;
+          return used(kt) ? static_cast<int>(ld_early(trow + ((kt * kKeys + 8 * grp) >> p.log2_block))) : -1;
         };
         auto block_of = [&](int kt, int e) -> int {
           if (e >= 0 && e < p.num_blocks) return e;
@@ -676,48 +684,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         auto scale_of = [&](const float* scales, int e) -> float {
           return e >= 0 ? __uint_as_float(ld_early(scales + static_cast<size_t>(e) * p.num_kv_heads + it.g)) : 0.f;
         };
-        const int raw0 = entry(0);
-        int raw_e = entry(1);
-        int e = block_of(0, raw0);
+        const int raw0 = entry(quad);
+        int raw_e = entry(4 + quad);
+        int e = block_of(quad, raw0);
         // (K's warp follows the V scales too: it tells the softmax both references)
         float sk = is_v ? 0.f : scale_of(p.k_scales, e), sv = scale_of(p.v_scales, e);
         float vref = 0.f;
-        for (int kt = 0; kt < n; ++kt, ++num) {
-          // the next item is claimed three tiles before this one's end: late, so that no SM
-          // sits on work that another could start, yet early enough for the answer
-          if (!is_v && kt == max(0, n - 3) && lane == 0) {
-            mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
-            claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
-          }
-          const int e1 = block_of(kt + 1, raw_e);
+        for (int base = 0; ok && base < n; base += 4) {
+          const int e1 = block_of(base + 4 + quad, raw_e);
           const float sk1 = is_v ? 0.f : scale_of(p.k_scales, e1), sv1 = scale_of(p.v_scales, e1);
-          raw_e = entry(kt + 2);
-          // (scales are positive, so their bits order as integers)
-          const float kref = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sk)));
-          const float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sv)));
-          if (kt == 0 || vtop > vref * kScaleRoom) vref = vtop;
-          const float ref = is_v ? vref : kref;
-          const float ratio = ref > 0.f ? (is_v ? sv : sk) * __frcp_rn(ref) : 0.f;
-          const int b = num & 1;
-          if (num >= 2 && !(ok = wwait(sm.raw_free[is_v][b], ((num >> 1) - 1) & 1))) break;
-          // free: the tile two back is read, with its ratios; K's tile three back is widened, so
-          // the P V of six back is done, and the softmax of 16 back is long done with its
-          // references
-          if (lane < kGroups) sm.ratio[is_v][b][lane] = ratio;
-          if (lane == 0 && !is_v) {
-            sm.kref[num & 15] = kref;
-            sm.vref[num & 15] = vref;
+          raw_e = entry(base + 8 + quad);
+          const float kmax = is_v ? 0.f : max8(sk), vmax = max8(sv);
+          for (int q = 0; q < 4 && base + q < n; ++q, ++num) {
+            // the next item is claimed three tiles before this one's end: late, so that no SM
+            // sits on work that another could start, yet early enough for the answer
+            if (!is_v && base + q == max(0, n - 3) && lane == 0) {
+              mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
+              claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
+            }
+            const float kref = __shfl_sync(0xffffffffu, kmax, 8 * q), vtop = __shfl_sync(0xffffffffu, vmax, 8 * q);
+            if (base + q == 0 || vtop > vref * kScaleRoom) vref = vtop;
+            const float ref = is_v ? vref : kref;
+            const float ratio = ref > 0.f ? (is_v ? sv : sk) * __frcp_rn(ref) : 0.f;
+            const bool mine_now = quad == q && first_group && e >= 0;  // (e < 0 past the groups)
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine_now)) * p.block_size * D;
+            const int b = num & 1;
+            if (num >= 2 && !(ok = wwait(sm.raw_free[is_v][b], ((num >> 1) - 1) & 1))) break;
+            // free: the tile two back is read, with its ratios; K's tile three back is widened, so
+            // the P V of six back is done, and the softmax of 16 back is long done with its
+            // references
+            if (quad == q) sm.ratio[is_v][b][grp] = ratio;
+            if (lane == 0 && !is_v) {
+              sm.kref[num & 15] = kref;
+              sm.vref[num & 15] = vref;
+            }
+            __syncwarp();  // the stores above before the arrival
+            if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]), bytes);
+            __syncwarp();
+            if (mine_now)
+              tma_load_4d(smem_addr(sm.raw[is_v][b]) + 8 * grp * D, is_v ? &p.vmap : &p.kmap, 0, 0, it.g, e,
+                          smem_addr(&sm.raw_full[is_v][b]));
           }
-          const bool mine_now = first_group && e >= 0;  // (e < 0 past the groups)
-          const uint32_t blocks = __ballot_sync(0xffffffffu, mine_now);
-          __syncwarp();  // the stores above before the arrival
-          if (lane == 0)
-            mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]),
-                                  static_cast<uint32_t>(__popc(blocks) * p.block_size * D));
-          __syncwarp();
-          if (mine_now)
-            tma_load_4d(smem_addr(sm.raw[is_v][b]) + 8 * lane * D, is_v ? &p.vmap : &p.kmap, 0, 0, it.g, e,
-                        smem_addr(&sm.raw_full[is_v][b]));
           e = e1;
           sk = sk1;
           sv = sv1;
