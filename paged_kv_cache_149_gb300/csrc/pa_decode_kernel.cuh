@@ -481,6 +481,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A piece of a cut pair as every holder of a piece sees it: the CTAs holding its first and
 // last pieces, where the first CTA stored its piece (slot 0 when the pair's family is that
 // CTA's first family), and the pair's sequence and heads.
@@ -1174,9 +1180,10 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       G = static_cast<int>(families);
       W = families * fw_min;
     } else {
-      const float steps = sqrtf(static_cast<float>(longest) * p.piece_cost);
-      const long long share = kWarps * static_cast<long long>(fmaxf(steps, 1.f));
-      if (W < share * G) G = static_cast<int>(max(1ll, W / share));
+      // (in floats and approximate instructions, the same in every CTA: integer divisions here
+      // are code that a cold instruction cache has to fetch)
+      const float steps = floorf(fmaxf(sqrt_approx(static_cast<float>(longest) * p.piece_cost), 1.f));
+      G = min(G, max(1, static_cast<int>(fminf(__fdividef(static_cast<float>(W), kWarps * steps), 1e6f))));
     }
     if (c >= G) return;  // (uniform over the CTA)
   }
@@ -1190,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   if constexpr (FB) {
     if (P > 1) {
       const long long families = static_cast<long long>(p.num_seqs) * p.ngroups;
-      narrow = 3 * max(1, static_cast<int>(min(families, static_cast<long long>(P) * G)) / G);
+      narrow = 3 * max(1, min(P, static_cast<int>(__fdividef(static_cast<float>(families), static_cast<float>(G)))));
     }
   }
   long long w0, w1;

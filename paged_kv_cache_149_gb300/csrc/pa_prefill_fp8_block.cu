@@ -1008,8 +1008,8 @@ int launch(const Params& prm, int max_query_len, int sm_count, cudaStream_t stre
   };
   long long count = items(kTiles);
   // Few items: one query tile each while every item still has an SM of its own.  One prompt
-  // of 128 / 512 tokens, 8 kv heads, 4 query heads each: 8.1 / 13.0 us, 10.2 / 15.1 us with
-  // two; a chunk of 512 over 2000 cached 39.1 us, 42.5 with two.  Past that, items queue: 8
+  // of 128 / 512 tokens, 8 kv heads, 4 query heads each: 8.4 / 13.1 us, 10.0 / 15.0 us with
+  // two; a chunk of 512 over 2000 cached 34.7 us, 41.5 with two.  Past that, items queue: 8
   // chunks of 100 over 1000 cached (128 items of two) 41.0 us, 25.0 with two.
   if (2 * count <= sm_count) count = items(1);
   if (count > 0x7fffffffLL) return -1;
