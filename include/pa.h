@@ -326,10 +326,12 @@ int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
  * decode(code) * scale of each token's block, and two more: num_tokens, the rows of q and out
  * (a sequence whose span lies outside them gets PA_DEVERR_BAD_CONTEXT and nothing is read
  * or written for it; rows behind the last sequence are not touched), and scale > 0.
- * Products run in f16: codes are widened relative to the largest scale near them, bf16 rows
- * of q brought to the type's upper range by a power of two, softmax weights rounded to f16;
- * accumulation fp32; outputs clamped as by pa_decode_fp8_block.  A NaN code reaches the tokens
- * that attend to it and no others.  Write the sequences' new tokens first
+ * Products run in f16 over the codes, widened exactly, and bf16 rows of q brought to the type's
+ * upper range by a power of two; K's scales multiply the fp32 scores, V's the softmax weights before
+ * they are rounded to f16, relative to the largest such product of the keys that the token attends
+ * to; accumulation fp32; outputs clamped as by pa_decode_fp8_block.  So a key that a token does
+ * not attend to changes none of its output's bits, whatever its codes and scales, and one that it
+ * attends to with next to no weight costs the others no precision.  Write the sequences' new tokens first
  * (pa_append_fp8_block). */
 int pa_prefill_fp8_block(const void* q, const void* k_cache, const void* v_cache,
                          const float* k_scales, const float* v_scales,

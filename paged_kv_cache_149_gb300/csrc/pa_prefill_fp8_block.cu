@@ -7,15 +7,15 @@
 //   out = sum_t softmax_t(scale <q, K_t>) V_t
 // (daiw.org "Paged Attention", section 回顾与衔接).
 //
-// Everything runs on the tensor cores in f16, whatever q's type: a code times a power of two
-// is exact there, the widening from E4M3 is one instruction for two values, and P keeps 11
-// bits.  Range is kept by references: a key tile's codes are widened to code * s / kref, kref
-// the tile's largest K scale, and its scores multiplied by kref where the softmax scales them
-// anyway; V's to code * s / vref, vref the largest V scale of the item's first tile (it moves,
-// with one rescale of O, only when a later scale is over 2^7 times it); each bf16 row of q
-// is multiplied by the power of two that brings its largest value to [2^14, 2^15).  For scales
-// that are powers of two no step rounds but those of values 2^-15 and more below their
-// reference (an absolute 2^-25 of it); other scales round each widened value once.
+// Everything runs on the tensor cores in f16, whatever q's type: an E4M3 code is exact there, the
+// widening is one instruction for two values, and P keeps 11 bits.  The scales stay out of the
+// operands, so no scale, of a key that a row attends to or of one that it does not, costs another
+// key's code a bit.  K's multiply the scores in the softmax, a factor per group of keys.  V's go
+// into the weights, 2^(z_t + log2 sV_t - r), r a reference of each row's own: the largest
+// z + log2 sV among the keys that it attends to (rounded up, moved when outgrown, with O), so that
+// f16 rounds weights where they count in O; the sum of weights takes the factor out again, group
+// by group.  (log2 sV is whole for the scales that the cache write stores.)  Each bf16 row of q is
+// multiplied by the power of two that brings its largest value to [2^14, 2^15).
 //
 // Design: persistent CTAs of 640 threads, one per SM; a work item is a (pair of 128-row query
 // tiles, sequence, kv head).  The grid has a CTA per item; a running CTA claims items of CTAs
@@ -26,8 +26,8 @@
 // items makes them one query tile each (see the launch).
 // * A query tile's rows are (token, query head of the kv head) pairs, 128 / G tokens x G
 //   heads; both tiles of the CTA share the key tiles (64 keys each).
-// * Two producer warps (K, V) look blocks and scales up four tiles at once, four ahead, and copy
-//   whole blocks of codes by TMA into two buffers each.
+// * Two producer warps (K, V) look blocks up four tiles at once, four ahead, and copy whole blocks
+//   of codes by TMA into two buffers each; K's also hands the softmax both scales of each group.
 // * Eight widening warps (four for K, four for V) turn codes into f16 in the swizzled layout
 //   that the tcgen05 descriptors read, into rings of kStages K and V tiles.  Rows past the
 //   context become zeros (what lies there is not used), and so do NaN codes of V from the first
@@ -38,17 +38,18 @@
 //   the S buffer, into 128 columns of O.  S of the next keys goes in before P V of the current
 //   ones, so each softmax finds its next scores ready.
 // * Two softmax warpgroups, one per query tile, one thread per row: the row's 64 scores in
-//   registers, mask, running maximum m and sum l in exp2 units, P.  O is rescaled only when a
-//   row's maximum grows by more than 15 (log2), so P <= 2^15 fits f16, whose smallest values
-//   only gain from it; the final O / l uses the same m.  (A limit of 8: 285 us, 15: 270 us for
-//   8 prompts of 2048 tokens whose blocks' scales spread over 2^4.)
+//   registers, mask, references m (of the scores) and r (of the scores with V's scale) and sum l in
+//   exp2 units, P.  O is rescaled only when a row outgrows r by more than 15 (log2) or m by 40, so
+//   P <= 2^15 fits f16, whose smallest values only gain from it; the final O / l uses the same.
+//   (A limit of 8: 285 us, 15: 270 us for 8 prompts of 2048 tokens whose blocks' scales spread
+//   over 2^4, before V's scales went into the weights.)
 // Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag.
 //
 // What bounds it: the softmax's step of 64 keys, about 1710 cycles against 1024 of tensor work,
 // at 1240 instructions a step on each of an SM's schedulers (mostly exponentials, maxima, sums
 // and the widening); then 5300 to 9000 cycles from an item's last P to the next item's first.
-// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 267 us (1030
-// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 188 us (995 TFLOP/s).  The 16-bit
+// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 272 us (1011
+// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 183 us (1022 TFLOP/s).  The 16-bit
 // prefill takes 292 and 202 us there.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -82,8 +83,14 @@ constexpr int kThreads = 32 * (kWidenWarp + 2 * kWidenWarps);
 constexpr int kSoftmaxRegs = 144;
 constexpr int kOtherRegs = 64;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescale = 15.f;     // log2 growth of a row's maximum that forces a rescale of O
-constexpr float kScaleRoom = 128.f; // growth of the largest V scale that moves vref
+constexpr float kRescale = 15.f;     // log2 growth past a row's r that forces a rescale of O, P <= 2^15
+constexpr float kLag = 40.f;         // past its m: fp32 sums of weights up to 2^40
+// Weights of groups with far smaller V scales than the row's largest are held up to 2^(z - m - kDeep),
+// at most 2^-40: zero in f16 P as they would be, and they still count in l.
+constexpr float kDeep = 80.f;
+constexpr float kLowest = -3e38f;    // the references of a row without a score
+constexpr float kLeast = 1e-37f;     // of a factor of the scores, which stays positive
+constexpr int kFactorSlots = 6;      // key tiles whose scale factors are kept: as many as can be under way
 
 struct Params {
   CUtensorMap kmap;  // codes as [num_blocks][Hkv][B][d] bytes, box (d, B, 1, 1)
@@ -167,11 +174,10 @@ struct Smem {
   uint8_t q[kTiles][kRows * D * 2];     // K-major, 128-byte swizzle; 1024-byte aligned
   uint8_t k[kStages][kKeys * D * 2];    // f16, [64-column half][64 keys][128 B]
   uint8_t v[kStages][kKeys * D * 2];
-  // [K, V][kt % 2]: codes as TMA lays them (128-byte swizzle at d = 128), and the groups'
-  // scales over their reference
-  uint8_t raw[2][2][kKeys * D];
-  float ratio[2][2][kGroups];
-  float kref[16], vref[16];            // of key tile number T (over all items) at T % 16
+  uint8_t raw[2][2][kKeys * D];         // [K, V][kt % 2]: codes as TMA lays them (128-byte swizzle at d = 128)
+  // of key tile number T (over all items) at T % kFactorSlots, per group of keys: K's scale times the
+  // softmax scale, and log2 of V's scale
+  float2 factor[kFactorSlots][kGroups];
   uint8_t stage[8][32 * 128];          // per softmax warp: 64 columns of its rows on their way out
   uint4 claim;                         // the answer to a claim
   Item item[kItems];
@@ -285,13 +291,12 @@ __device__ __forceinline__ int claim_answer(uint32_t from) {
   return ok ? static_cast<int>(x) : -1;
 }
 
-// Eight codes (two words) times a ratio -> eight f16 values.
-__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __half2 ratio) {
+// Eight codes (two words) -> eight f16 values.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
   auto two = [&](uint32_t c) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-    const __half2 w = __hmul2(*reinterpret_cast<__half2*>(&h), ratio);
-    return *reinterpret_cast<const uint32_t*>(&w);
+    return h;
   };
   return make_uint4(two(lo), two(lo >> 16), two(hi), two(hi >> 16));
 }
@@ -308,6 +313,23 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ float2 ld_shared8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+// 8 or 4 columns (packed f16 pairs) written to this thread's TMEM lane.
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
 // A 32-bit load of data that no kernel of the call writes, kept at its place in the program.
@@ -349,12 +371,14 @@ __device__ __forceinline__ float q_row_to_f16(uint32_t tile, int r) {
   return __uint_as_float(static_cast<uint32_t>(254 - fe) << 23);
 }
 
-template <int D, typename T>
+// NG: groups of keys with a scale in a key tile: of 16 keys, or of 8 where blocks are as short.
+template <int D, typename T, int NG>
 __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __grid_constant__ Params p) {
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   constexpr int CH = D / 8;        // 16-byte chunks of a 16-bit row
   constexpr int KS1 = D / 16;      // MMA k-steps of S = Q K^T
   constexpr int KS2 = kKeys / 16;  // MMA k-steps of P V
+  constexpr int GK = kKeys / NG;   // keys of a scale group
   constexpr uint32_t kTileCols = 256;  // TMEM columns per query tile:
   constexpr uint32_t kColS = kKeys;    //   S of key tile kt in [64 (kt % 2), + 64), its P over the
   constexpr uint32_t kColO = 128;      //   first 32 of those columns, O in [128, 128 + D)
@@ -438,10 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp >= kWidenWarp) {
       // ===== widening: K (or V) tiles of the rings =====
-      // Warp cw takes rows 16 cw .. 16 cw + 15 of each tile, two groups of eight tokens (eight
-      // tokens never straddle a block, so a group has one scale).  At d = 128 a lane takes
-      // 16-byte chunk (lane % 4) + 4 hc of one row of the group: eight lanes cover four chunks
-      // of rows r and r ^ 5, which makes both the swizzled code loads and the swizzled f16
+      // Warp cw takes rows 16 cw .. 16 cw + 15 of each tile, two groups of eight tokens.  At
+      // d = 128 a lane takes 16-byte chunk (lane % 4) + 4 hc of one row of the group: eight lanes
+      // cover four chunks of rows r and r ^ 5, which makes both the swizzled code loads and the swizzled f16
       // stores (chunks 2 c and 2 c + 1 of the same row) free of bank conflicts.  At d = 64 a
       // warp covers the group's eight rows of four chunks at once.
       constexpr int NH = D / 64;  // instructions per group
@@ -478,7 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         for (int kt = 0; kt < n; ++kt, ++num, r3.next()) {
           const int b = num & 1;
           if (!(ok = wwait(sm.raw_full[is_v][b], (num >> 1) & 1))) break;
-          const float2 r = *reinterpret_cast<const float2*>(&sm.ratio[is_v][b][2 * cw]);
           uint4 c[2][NH];
 #pragma unroll
           for (int gi = 0; gi < 2; ++gi)
@@ -519,12 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           const uint32_t tile = ring + r3.st * (kKeys * D * 2);
 #pragma unroll
           for (int gi = 0; gi < 2; ++gi) {
-            const __half2 ratio = __float2half2_rn(gi ? r.y : r.x);
 #pragma unroll
             for (int hc = 0; hc < NH; ++hc) {
               const uint32_t at = tile + 8 * gi * 128 + hc * (kKeys * 128);
-              st_shared16(at + put0, widen8(c[gi][hc].x, c[gi][hc].y, ratio));
-              st_shared16(at + put1, widen8(c[gi][hc].z, c[gi][hc].w, ratio));
+              st_shared16(at + put0, widen8(c[gi][hc].x, c[gi][hc].y));
+              st_shared16(at + put1, widen8(c[gi][hc].z, c[gi][hc].w));
             }
           }
           fence_async_smem();  // these stores before the tensor cores' reads
@@ -605,11 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       // softmax's step.)
       const int grp = lane & 7, quad = lane >> 3;
       const bool first_group = ((8 * grp) & (p.block_size - 1)) == 0;  // of its block
-      auto max8 = [&](float x) -> float {  // over the lanes of a tile; scales are positive
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        return x;
-      };
       uint32_t num = 0, claims = 0, loads = 0;  // key tiles, claims and q loads so far
       Item it;
       if (!is_v) it = item_of(blockIdx.x);
@@ -687,14 +703,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         const int raw0 = entry(quad);
         int raw_e = entry(4 + quad);
         int e = block_of(quad, raw0);
-        // (K's warp follows the V scales too: it tells the softmax both references)
-        float sk = is_v ? 0.f : scale_of(p.k_scales, e), sv = scale_of(p.v_scales, e);
-        float vref = 0.f;
+        float sk = 0.f, sv = 1.f;  // (K's warp: it tells the softmax both)
+        auto scales_of = [&](int b) {
+          if (is_v) return;
+          sk = scale_of(p.k_scales, b);
+          sv = scale_of(p.v_scales, b);
+        };
+        scales_of(e);
         for (int base = 0; ok && base < n; base += 4) {
           const int e1 = block_of(base + 4 + quad, raw_e);
-          const float sk1 = is_v ? 0.f : scale_of(p.k_scales, e1), sv1 = scale_of(p.v_scales, e1);
+          // (bf16: kept positive with the row's factor)
+          const float kf = BF ? sk * p.scale_log2 : fmaxf(sk * p.scale_log2, kLeast), vl = __log2f(sv);
+          scales_of(e1);
           raw_e = entry(base + 8 + quad);
-          const float kmax = is_v ? 0.f : max8(sk), vmax = max8(sv);
           for (int q = 0; q < 4 && base + q < n; ++q, ++num) {
             // the next item is claimed three tiles before this one's end: late, so that no SM
             // sits on work that another could start, yet early enough for the answer
@@ -702,22 +723,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
               mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
               claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
             }
-            const float kref = __shfl_sync(0xffffffffu, kmax, 8 * q), vtop = __shfl_sync(0xffffffffu, vmax, 8 * q);
-            if (base + q == 0 || vtop > vref * kScaleRoom) vref = vtop;
-            const float ref = is_v ? vref : kref;
-            const float ratio = ref > 0.f ? (is_v ? sv : sk) * __frcp_rn(ref) : 0.f;
             const bool mine_now = quad == q && first_group && e >= 0;  // (e < 0 past the groups)
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine_now)) * p.block_size * D;
             const int b = num & 1;
             if (num >= 2 && !(ok = wwait(sm.raw_free[is_v][b], ((num >> 1) - 1) & 1))) break;
-            // free: the tile two back is read, with its ratios; K's tile three back is widened, so
-            // the P V of six back is done, and the softmax of 16 back is long done with its
-            // references
-            if (quad == q) sm.ratio[is_v][b][grp] = ratio;
-            if (lane == 0 && !is_v) {
-              sm.kref[num & 15] = kref;
-              sm.vref[num & 15] = vref;
-            }
+            // free: the tile two back is read; K's tile three back is widened, so the P V of six back
+            // is done, and the softmax of kFactorSlots back with its factors
+            if (quad == q && !is_v && grp % (8 / NG) == 0)
+              sm.factor[num % kFactorSlots][grp / (8 / NG)] = make_float2(kf, vl);
             __syncwarp();  // the stores above before the arrival
             if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]), bytes);
             __syncwarp();
@@ -726,8 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
                           smem_addr(&sm.raw_full[is_v][b]));
           }
           e = e1;
-          sk = sk1;
-          sv = sv1;
         }
         if (!ok) break;
         if (!is_v) {
@@ -838,19 +849,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       const int tok = it.tok0 + t * tpt + tile_tok;
       const int pos = tile_tok < tpt && tok < it.end ? it.ctx - it.qlen + tok : -1;
       const int pos_lo = it.ctx - it.qlen + it.tok0 + t * tpt;  // the tile's first position
-      float m_used = -INFINITY, l_run = 0.f, vref = 0.f;
-      float row_scale = p.scale_log2;  // of this row's scores, before the key tile's kref
+      // (log2) references of the scores and of the scores with V's scales, and the sum of weights
+      float m_ref = 0.f, r_ref = 0.f, l_run = 0.f;
+      float q_fac = 1.f;  // turns this row's scores back
       for (int kt = 0; kt < ntt; ++kt, ++sn) {
         const int b = sn & 1;
-        // (kref and vref were written before k_full of this tile, q_factor before q_ready, which
+        // (the factors were written before k_full of this tile, q_factor before q_ready, which
         // the MMA warp acquired before it arrived here)
         if (!(ok = wwait(sm.s_full[t][b], (sn >> 1) & 1))) break;
         tc_fence_after();
-        if (BF && kt == 0) row_scale *= sm.q_factor[t][r];
-        // the tile's factor of the raw scores, positive (so that the maximum commutes with it
-        // and a masked -inf stays -inf even where it would underflow)
-        const float c = fmaxf(sm.kref[(num + kt) & 15] * row_scale, 1e-37f);
-        const float vnew = sm.vref[(num + kt) & 15];
+        if (BF && kt == 0) q_fac = sm.q_factor[t][r];
+        const uint32_t factor = smem_addr(sm.factor[(num + kt) % kFactorSlots]);
+        // group g's factor of the raw scores, positive (so that the maximum commutes with it and a
+        // masked -inf stays -inf even where it would underflow), and log2 of its V scale; read
+        // where they are used, twice, since the 64 scores leave few registers
+        auto factors = [&](int g) -> float2 {
+          float2 f = ld_shared8(factor + 8 * g);
+          if (BF) f.x = fmaxf(f.x * q_fac, kLeast);
+          return f;
+        };
         float sv[kKeys];
         tmem_get64(tl + b * kColS, sv);
         if (kt * kKeys + kKeys - 1 > pos_lo) {  // causal mask: key kt * 64 + i > pos
@@ -859,76 +876,94 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           for (int i = 0; i < kKeys; ++i)
             if (i > lim) sv[i] = -INFINITY;
         }
-        float pm[4];  // four chains of three-input maxima
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) pm[q] = fmaxf(sv[2 * q], sv[2 * q + 1]);
+        for (int g = 0; g < NG; g += 2) {
+          float m[2], y[2];
 #pragma unroll
-        for (int i = 8; i < kKeys; i += 8)
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = factors(g + k);
+            const float* x = sv + (g + k) * GK;
+            m[k] = fmaxf(x[0], x[1]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) pm[q] = fmax3(pm[q], sv[i + 2 * q], sv[i + 2 * q + 1]);
-        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-        const float m_new = fmaxf(m_used, mx * c);
-        const bool need = kt > 0 && m_new > m_used + kRescale;
-        const bool moved = kt > 0 && vnew != vref;  // (uniform over the CTA)
-        if (moved || __any_sync(0xffffffffu, need)) {
-          // rescale O, once P V of the tile before is done (the one before that was issued
-          // before this S)
-          if (!(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
-          tc_fence_after();
-          float alpha = need ? ex2(m_used - m_new) : 1.f;
-          if (need) {
-            l_run *= alpha;
-            m_used = m_new;
+            for (int i = 2; i < GK; i += 2) m[k] = fmax3(m[k], x[i], x[i + 1]);
+            m[k] *= f.x;
+            y[k] = m[k] + f.y;
           }
-          if (moved) alpha *= vref / vnew;
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_get32(tl + kColO + c0, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(tl + kColO + c0, o);
-          }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          mx = fmax3(mx, m[0], m[1]);
+          my = fmax3(my, y[0], y[1]);
         }
-        if (kt == 0) m_used = m_new;
-        vref = vnew;
-        // P = 2^(s c - m), rounded to f16, packed two a column over the first half of this
-        // thread's own row of S (already in registers); a row with nothing unmasked yet has
-        // every score at -inf, so any finite offset gives it P = 0
-        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
-        float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                        make_float2(0.f, 0.f)};
+        // (whole references, so that they and whole log2 scales add exactly)
+        if (kt == 0) {
+          m_ref = mx > -INFINITY ? ceilf(mx) : kLowest;
+          r_ref = my > -INFINITY ? ceilf(my) : kLowest;
+        } else {
+          const bool need = mx > m_ref + kLag || my > r_ref + kRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            // rescale O, once P V of the tile before is done (the one before that was issued
+            // before this S)
+            if (!(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
+            tc_fence_after();
+            float alpha = 1.f;
+            if (need) {
+              const float m_new = fmaxf(m_ref, ceilf(mx)), r_new = fmaxf(r_ref, ceilf(my));
+              l_run *= ex2(m_ref - m_new);
+              alpha = ex2(r_ref - r_new);
+              m_ref = m_new;
+              r_ref = r_new;
+            }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[16];
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              float o[32];
+              tmem_get32(tl + kColO + c0, o);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 x = __ffma2_rn(make_float2(sv[32 * h + i], sv[32 * h + i + 1]), c2, nm2);
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(tl + kColO + c0, o);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
+        }
+        // P = 2^(s c + log2 sV - r), rounded to f16, packed two a column over the first half of this
+        // thread's own row of S (already in registers); its unrounded sum, without the V scale, in l.
+        // (the factors are read again and P leaves group by group: held in registers beside the 64
+        // scores they spilled, 297 us for 8 prompts of 2048 tokens, 272 so)
+        float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 f = factors(g);
+          const float a = fmaxf(f.y - r_ref, -kDeep - m_ref);
+          const float2 c2 = make_float2(f.x, f.x), a2 = make_float2(a, a);
+          float2 ps[2];
+          uint32_t pk[GK / 2];
+#pragma unroll
+          for (int i = 0; i < GK; i += 2) {
+            const float2 x = __ffma2_rn(make_float2(sv[g * GK + i], sv[g * GK + i + 1]), c2, a2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
-            ps[(i >> 1) & 3] = __fadd2_rn(ps[(i >> 1) & 3], e);
+            ps[(i >> 1) & 1] = i < 4 ? e : __fadd2_rn(ps[(i >> 1) & 1], e);
             pk[i >> 1] = pack2<__half>(e.x, e.y);
           }
-          tmem_st16(tl + b * kColS + 16 * h, pk);
+          const float2 sum = __fadd2_rn(ps[0], ps[1]);
+          const float w = ex2(-a - m_ref);
+          l2 = __ffma2_rn(sum, make_float2(w, w), l2);
+          tmem_put(tl + b * kColS + g * (GK / 2), pk);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();  // the P stores before the MMA warp reads them
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[t][b]));
-        const float2 s01 = __fadd2_rn(ps[0], ps[1]), s23 = __fadd2_rn(ps[2], ps[3]);
-        const float2 sall = __fadd2_rn(s01, s23);
-        l_run += sall.x + sall.y;
+        l_run += l2.x + l2.y;
       }
       if (!ok) break;
       if (ntt > 0 && !(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
       tc_fence_after();
       num += n;
-      // ---- out = O vref / l (the item's tiles are done, so its bad-block flag is final) ----
+      // ---- out = O 2^(r - m) / l (the item's tiles are done, so its bad-block flag is final) ----
       const bool good = it.run == 1 && ntt > 0 && *reinterpret_cast<volatile int*>(&sm.item[j % kItems].bad) == 0;
       const bool nan = good && *reinterpret_cast<volatile int*>(&sm.item[j % kItems].nan) != 0;
       item_done(j);
-      const float inv = vref / l_run;
+      // (in two steps, each a float where r - m is near the exponents' ends)
+      const float lift = r_ref > m_ref ? 16.f : -16.f;
+      const float inv = ex2(r_ref - m_ref - lift) / l_run * ex2(lift);
       // The rows go out through shared memory, 64 columns at a time, so that each store
       // instruction of a warp writes whole 128-byte lines.  Row r's 16-byte chunk c sits at
       // chunk c ^ (r % 8) of its 128-byte staging row: neither the writes nor the reads
@@ -991,10 +1026,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
   }
 }
 
-template <int D, typename T>
+template <int D, typename T, int NG>
 int launch(const Params& prm, int max_query_len, int sm_count, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<D>) + 1024;
-  auto* kern = prefill_fp8_block_kernel<D, T>;
+  auto* kern = prefill_fp8_block_kernel<D, T, NG>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return -3;
   cudaLaunchConfig_t cfg = {};
   // query blocks, whatever the lengths are: a part of one per sequence beyond the whole ones
@@ -1056,12 +1091,15 @@ int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* 
   p.scale_log2 = a.scale * prefill8::kLog2e;
   p.q_tma = q_tile_map(&p.qmap, a.q, a.num_q_heads, a.head_dim, p.group, num_tokens) ? 1 : 0;
   p.err = a.err;
-  if (a.head_dim == 128)
-    return a.bf16 ? prefill8::launch<128, __nv_bfloat16>(p, a.max_query_len, sm_count, stream)
-                  : prefill8::launch<128, __half>(p, a.max_query_len, sm_count, stream);
-  if (a.head_dim == 64)
-    return a.bf16 ? prefill8::launch<64, __nv_bfloat16>(p, a.max_query_len, sm_count, stream)
-                  : prefill8::launch<64, __half>(p, a.max_query_len, sm_count, stream);
+#define PA_PREFILL_CASE(DD, NN)                                                            \
+  if (a.head_dim == DD && (a.block_size == 8) == (NN == 8))                                \
+    return a.bf16 ? prefill8::launch<DD, __nv_bfloat16, NN>(p, a.max_query_len, sm_count, stream) \
+                  : prefill8::launch<DD, __half, NN>(p, a.max_query_len, sm_count, stream);
+  PA_PREFILL_CASE(128, 4)
+  PA_PREFILL_CASE(128, 8)
+  PA_PREFILL_CASE(64, 4)
+  PA_PREFILL_CASE(64, 8)
+#undef PA_PREFILL_CASE
   return -1;
 }
 

@@ -130,8 +130,8 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 2^x by the special-function unit (approximate, subnormal results flushed to zero; the
-// arguments here are <= 8 and results below 2^-126 only lose weights that small).
+// 2^x by the special-function unit (approximate, subnormal results flushed to zero: where the
+// softmaxes take it of a weight they lose weights that small).
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
