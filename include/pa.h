@@ -313,7 +313,8 @@ int pa_append_fp8_block(const void* key, const void* value, void* k_cache, void*
  * out are fp16 or bf16 (`dtype`).  The codes are widened to f16 exactly and multiplied on the
  * tensor cores in f16 (bf16 queries rounded to f16, so |q| < 65520); the K scale multiplies
  * the fp32 scores, the V scale the softmax weights before they are rounded to f16, relative
- * to the largest V scale met so far, so that its size does not matter; accumulation fp32;
+ * to the largest such product (weight times V scale), so that f16 loses 2^-25 of that at most,
+ * and a large V scale of a token with next to no weight costs the others nothing; accumulation fp32;
  * outputs past the type's largest value are clamped to it (a cached 65504 is held as 65536).
  * Same workspace, ordering, error and determinism rules as pa_decode. */
 int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,

@@ -481,6 +481,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Where the largest score met starts over FP8 blocks with block scales: below any score, and a
+// float whose differences are numbers.
+constexpr float kLowest = -3e38f;
+
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1069,10 +1073,12 @@ __device__ __forceinline__ bool next_busy_fam(Fam f, int pi, int phase, int narr
 // KV = kKvFp8Block: E4M3 codes with a float32 scale per (block, kv head).  Eight tokens never
 // straddle a block, so a stage has four groups of tokens with one K and one V scale each,
 // and a lane's scores of one (m-tile, half) lie in one group: the K scale is one factor of
-// each score.  The V scale vs multiplies the weights before they are rounded to f16 for P V,
-// relative to the largest scale V_ref that the warp has met (2^-k <= 1, exact for the powers
-// of two that the cache write stores), so that no scale over- or underflows f16; O holds
-// sums over V_ref, rescaled with the running maximum when V_ref grows.
+// each score z (log2).  The V scale goes into the weights that P V rounds to f16: 2^(z + log2 sV - r),
+// r each head's largest z + log2 sV so far, rounded up (with log2 sV whole, as the cache write's
+// powers of two are, the difference is exact).  So f16 rounds weights where they count in O, and
+// neither a scale nor a token without weight costs another token's bits.  The sum of the weights
+// themselves is each lane's own, against the largest score that the lane has met: it needs no
+// exchange until the pair's end.
 // KV = kKvInt4: K/V blocks hold INT4 codes with a float32 scale per row: a token's K scale
 // multiplies its scores, its V scale its weights in P V.  Both quantised formats run the
 // MMAs in f16 on values widened exactly, with 32-token stages and the permuted d order of
@@ -1504,18 +1510,18 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     }
 
     // This lane's softmax columns: heads 8*nt + qc and + 1 of every n-tile.
-    float m_run[NTH][2], l_run[NTH][2];
+    // (FB: m and l of this lane's tokens alone, r_run of the whole column)
+    float m_run[NTH][2], l_run[NTH][2], r_run[NTH][2];
     float o[MT][NTH][4];  // O^T: rows d = 16*mt + r0 (+8), columns = heads
 #pragma unroll
     for (int nt = 0; nt < NTH; ++nt) {
-      m_run[nt][0] = m_run[nt][1] = -INFINITY;
+      m_run[nt][0] = m_run[nt][1] = FB ? kLowest : -INFINITY;
+      r_run[nt][0] = r_run[nt][1] = kLowest;
       l_run[nt][0] = l_run[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
     bool seg_bad = false;
-    // FB: the largest V scale met so far (O holds sums over it), and its reciprocal
-    float v_ref = 0.f, v_inv = 0.f;
 
     const int j_first = alone ? r.x : r.x + (phase - r.x % P + P) % P;
     for (int j = j_first; j < r.y; j += alone ? 1 : P) {
@@ -1600,26 +1606,14 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
               vsc[u][hr] = lds_f32(sa + G_::kScaleBytes);
             }
         }
-        // FB: the K scale (with the softmax scale) and the relative V scale of the tokens
-        // 16u + 8 hr .. + 7, and the factor that brings O to a grown V_ref
-        float bks[U][2], bvs[U][2], v_fac = 1.f;
+        // FB: log2 of the V scale of the tokens 16u + 8 hr .. + 7
+        float vlog[U][2];
         if constexpr (FB) {
-          const float4 sk = *reinterpret_cast<const float4*>(&sm.bscale[warp][slot][0]);
           const float4 sv = *reinterpret_cast<const float4*>(&sm.bscale[warp][slot][4]);
-          const float top = fmaxf(v_ref, fmaxf(fmaxf(sv.x, sv.y), fmaxf(sv.z, sv.w)));
-          if (top > v_ref) {  // (uniform over the warp)
-            v_inv = __frcp_rn(top);
-            v_fac = v_ref * v_inv;
-            v_ref = top;
-          }
-          bks[0][0] = sk.x * p.scale_log2;
-          bks[0][1] = sk.y * p.scale_log2;
-          bks[U - 1][0] = sk.z * p.scale_log2;
-          bks[U - 1][1] = sk.w * p.scale_log2;
-          bvs[0][0] = sv.x * v_inv;
-          bvs[0][1] = sv.y * v_inv;
-          bvs[U - 1][0] = sv.z * v_inv;
-          bvs[U - 1][1] = sv.w * v_inv;
+          vlog[0][0] = __log2f(sv.x);
+          vlog[0][1] = __log2f(sv.y);
+          vlog[U - 1][0] = __log2f(sv.z);
+          vlog[U - 1][1] = __log2f(sv.w);
         }
         if constexpr (I4) {
           // K rows 16u + r0 and + 8, bytes [(D/8) t, (D/8)(t+1)): word j holds the eight d
@@ -1716,6 +1710,15 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
         float alpha[NTH][2];
 #pragma unroll
         for (int nt = 0; nt < NTH; ++nt) {
+          // FB: the K scale (with the softmax scale) of the tokens 16u + 8 hr .. + 7
+          float bks[U][2];
+          if constexpr (FB) {
+            const float4 sk = *reinterpret_cast<const float4*>(&sm.bscale[warp][slot][0]);
+            bks[0][0] = sk.x * p.scale_log2;
+            bks[0][1] = sk.y * p.scale_log2;
+            bks[U - 1][0] = sk.z * p.scale_log2;
+            bks[U - 1][1] = sk.w * p.scale_log2;
+          }
           float x[U][4];
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -1733,6 +1736,27 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
             float mx = fmaxf(x[0][cc], x[0][cc + 2]);
 #pragma unroll
             for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(x[u][cc], x[u][cc + 2]));
+            if constexpr (FB) {
+              float my = fmaxf(x[0][cc] + vlog[0][0], x[0][cc + 2] + vlog[0][1]);
+#pragma unroll
+              for (int u = 1; u < U; ++u)
+                my = fmaxf(my, fmaxf(x[u][cc] + vlog[u][0], x[u][cc + 2] + vlog[u][1]));
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 4));
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 8));
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 16));
+              const float r_new = fmaxf(r_run[nt][cc], ceilf(my)), m_new = fmaxf(m_run[nt][cc], mx);
+              alpha[nt][cc] = fast_exp2(r_run[nt][cc] - r_new);
+              l_run[nt][cc] *= fast_exp2(m_run[nt][cc] - m_new);
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                l_run[nt][cc] += fast_exp2(x[u][cc] - m_new) + fast_exp2(x[u][cc + 2] - m_new);
+                pr[u][cc] = fast_exp2(x[u][cc] + (vlog[u][0] - r_new));
+                pr[u][cc + 2] = fast_exp2(x[u][cc + 2] + (vlog[u][1] - r_new));
+              }
+              r_run[nt][cc] = r_new;
+              m_run[nt][cc] = m_new;
+              continue;
+            }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -1757,8 +1781,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           for (int u = 0; u < U; ++u) {
             // (INT4: each token's weight times its V scale; the sums l keep the weights,
             // W the rounded products that enter P V)
-            const float v0 = I4 ? vsc[u][0] : (FB ? bvs[u][0] : 1.f);
-            const float v1 = I4 ? vsc[u][1] : (FB ? bvs[u][1] : 1.f);
+            const float v0 = I4 ? vsc[u][0] : 1.f, v1 = I4 ? vsc[u][1] : 1.f;
             const uint32_t w01 = pack2<TM>(pr[u][0] * v0, pr[u][1] * v0);  // tokens 16u + 0-7
             const uint32_t w23 = pack2<TM>(pr[u][2] * v1, pr[u][3] * v1);  // tokens 16u + 8-15
             if constexpr (I4) {
@@ -1772,13 +1795,6 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           if constexpr (I4) {
             wsum[nt][0] = fmaf(wsum[nt][0], alpha[nt][0], wst0);
             wsum[nt][1] = fmaf(wsum[nt][1], alpha[nt][1], wst1);
-          }
-        }
-        if constexpr (FB) {
-#pragma unroll
-          for (int nt = 0; nt < NTH; ++nt) {
-            alpha[nt][0] *= v_fac;
-            alpha[nt][1] *= v_fac;
           }
         }
         bool all_one = true;
@@ -1931,13 +1947,29 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     }
     const bool whole = r.x == 0 && r.y == f.ns;
     if constexpr (FB) {
-      // O in the values' own units (pieces and the warps of a pair have V_refs of their own)
+      // The column's m (whole) and l from its lanes', and O against m in r's place.
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NTH; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NTH; ++nt)
+        for (int cc = 0; cc < 2; ++cc) {
+          float m = m_run[nt][cc];
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = ceilf(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)));
+          float l = l_run[nt][cc] * fast_exp2(m_run[nt][cc] - m);
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          const bool none = m <= kLowest;  // no units, or no score that is a number
+          const float f = none ? 1.f : exp2f(r_run[nt][cc] - m);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= v_ref;
+          for (int mt = 0; mt < MT; ++mt) {
+            o[mt][nt][cc] *= f;
+            o[mt][nt][cc + 2] *= f;
+          }
+          m_run[nt][cc] = none ? -INFINITY : m;
+          l_run[nt][cc] = l;
+        }
     }
     const int slot_out = cta_first ? 0 : 1;
     const size_t piece = (static_cast<size_t>(c) * 2 + slot_out) * p.gs + pi;

@@ -181,3 +181,43 @@ def test_prefill_over_the_whole_range_of_scales(low, high):
     got, q, qs = prefill(b, caches, q_bits, [150], 0.09)
     assert np.isfinite(got).all()
     check(b, caches, got, q, qs, 0.09, rows=(0, 15, 31, 32, 40, 64, 100, 149))
+
+
+# ------------------------------------------------------------------------------ decode
+
+def decode(b, caches, q_bits, scale):
+    out = pa.decode_fp8_block(dev16(q_bits, b.dtype), *upload(caches), dev(b.tables), dev(b.ctx), scale)
+    assert device_error() == 0
+    return values(out, b.dtype), decode_bits(q_bits, b.dtype), np.arange(len(b.ctx) + 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("B,hq,hkv,d", [(8, 8, 8, 64), (16, 8, 2, 128), (32, 16, 1, 128), (16, 32, 8, 128)])
+@pytest.mark.parametrize("ctx", [150, 3000])
+@pytest.mark.parametrize("far,grow", [(60, 30), (20, 22), (12, 14)])
+def test_decode_of_a_large_block_without_weight(dtype, B, hq, hkv, d, ctx, far, grow):
+    """A block whose V scale is larger by 2^grow and whose weight is e^-far of the others', in
+    sequences of one piece and of many."""
+    b, q_row, caches = negligible(dtype, B, hq, hkv, d, ctx, far, far)
+    for s in range(2):
+        caches[3][b.tables[s, 2]] *= np.float32(2.0 ** grow)
+    q_bits = encode_bits(np.broadcast_to(q_row, (2, hq, d)).copy(), dtype)
+    got, q, qs = decode(b, caches, q_bits, 1.0)
+    check(b, caches, got, q, qs, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("B,hq,hkv,d", [(8, 8, 8, 64), (16, 8, 2, 128), (32, 16, 1, 128), (16, 7, 1, 64)])
+@pytest.mark.parametrize("ctx", [[130, 7, 33], [2500]])
+def test_decode_over_scales_at_random(dtype, B, hq, hkv, d, ctx):
+    """V scales over 2^-40 .. 2^40 and K scales over 2^8, block by block, in no order."""
+    b = Batch(ctx, hq, hkv, d, B, dtype, seed=d + B)
+    caches = [x.copy() for x in b.written()]
+    low, high = (-40, 41) if dtype == "bf16" else (-6, 7)
+    for s, c in enumerate(ctx):
+        for blk in b.tables[s, :-(-c // B)]:
+            caches[3][blk] *= np.exp2(b.rng.integers(low, high, hkv)).astype(np.float32)
+            caches[2][blk] *= np.exp2(b.rng.integers(-8, 1, hkv)).astype(np.float32)
+    q_bits = rows16(b.rng, (len(ctx), hq, d), dtype)
+    got, q, qs = decode(b, caches, q_bits, 1.0 / np.sqrt(d))
+    check(b, caches, got, q, qs, 1.0 / np.sqrt(d))
