@@ -221,3 +221,39 @@ def test_decode_over_scales_at_random(dtype, B, hq, hkv, d, ctx):
     q_bits = rows16(b.rng, (len(ctx), hq, d), dtype)
     got, q, qs = decode(b, caches, q_bits, 1.0 / np.sqrt(d))
     check(b, caches, got, q, qs, 1.0 / np.sqrt(d))
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (4, 1), (16, 1)])
+@pytest.mark.parametrize("ctx", [100, 2600])
+@pytest.mark.parametrize("low,high", [(-100, 120), (-140, -126), (-130, 90), (100, 120)])
+def test_decode_over_the_whole_range_of_scales(hq, hkv, ctx, low, high):
+    """bf16 outputs over V scales that alternate between the ends of the range that the write
+    stores, and past it (subnormal floats, in a cache made elsewhere); the first sequence has the
+    lower end alone."""
+    b = Batch([30, ctx], hq, hkv, 128, 16, "bf16", seed=7)
+    caches = [x.copy() for x in b.written()]
+    np.copyto(caches[1], caches[1] & 0xBF, where=(caches[1] & 0x7F) != 0x7F)  # (codes below 2)
+    for s in range(2):
+        for j in range(-(-int(b.ctx[s]) // 16)):
+            caches[3][b.tables[s, j]] = np.float32(2.0 ** (low if (j // 2) % 2 == 0 else high))
+    q_bits = rows16(b.rng, (2, hq, 128), "bf16")
+    got, q, qs = decode(b, caches, q_bits, 0.09)
+    assert np.isfinite(got).all()
+    check(b, caches, got, q, qs, 0.09)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (4, 1), (32, 2)])
+@pytest.mark.parametrize("ctx", [40, 3000])
+def test_decode_of_values_whose_sum_passes_fp32(hq, hkv, ctx):
+    """Values near bf16's largest: their sum over the context is no float, their average is."""
+    b = Batch([ctx], hq, hkv, 64, 16, "bf16", seed=3)
+    b.value[:] = np.where(b.value & 0x8000, 0xFEC0, 0x7EC0)  # +-1.5 * 2^126
+    caches = b.written()
+    q_bits = rows16(b.rng, (1, hq, 64), "bf16")
+    got, q, qs = decode(b, caches, q_bits, 0.125)
+    assert np.isfinite(got).all()
+    check(b, caches, got, q, qs, 0.125)
+    b.value[:] = 0x7F00  # 2^127
+    caches = b.written()
+    got, q, qs = decode(b, caches, q_bits, 0.125)
+    check(b, caches, got, q, qs, 0.125)
