@@ -191,6 +191,20 @@ __device__ __forceinline__ uint32_t pack2_sat<__half>(float a, float b) {
   return r;
 }
 
+// bf16 queries enter f16 products times the power of two that brings the largest of them
+// (magnitude bits `top`) to [2^14, 2^15), so that f16 loses at most 2^-39 of that value whatever its
+// size.  The exponent field of that power, at most 2^113 (for queries below 2^-99), and 1 where
+// the largest is not finite; that of its inverse is 254 less this.
+__device__ __forceinline__ int q_lift(uint32_t top) {
+  const int e = static_cast<int>(top >> 7);  // exponent field, bias 127
+  return e == 255 ? 127 : min(240, 127 + 14 - (e - 127));
+}
+// Two bf16 values times f -> two f16 values.
+__device__ __forceinline__ uint32_t q_lifted(uint32_t w, float f) {
+  const float2 x = unpack2<__nv_bfloat16>(w);
+  return pack2<__half>(x.x * f, x.y * f);
+}
+
 // One float -> one 16-bit value, round to nearest even.
 template <typename T>
 __device__ __forceinline__ T from_float(float v);

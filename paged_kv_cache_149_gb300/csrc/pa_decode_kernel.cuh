@@ -1001,8 +1001,8 @@ __device__ __forceinline__ void load_q(const Params& p, int s, int h0, int nh, i
 // The same for FP8 blocks, as f16 (the type the E4M3 values are widened to), with d in the
 // order the K fragments use: k-step ks takes d = (D/4) t + 4 ks + {0, 1} into b0 and
 // + {2, 3} into b1, t = lane % 4.  bf16 queries are rounded to f16 (exact within the f16
-// normal range).
-template <int D, int NTH, typename T>
+// normal range), or left as they are for lift_q8.
+template <int D, int NTH, typename T, bool AS_IS>
 __device__ __forceinline__ void load_q8(const Params& p, int s, int h0, int nh, int lane,
                                         uint32_t (&qb)[D / 16][NTH][2]) {
   const int r0 = lane >> 2, t = lane & 3;
@@ -1015,7 +1015,7 @@ __device__ __forceinline__ void load_q8(const Params& p, int s, int h0, int nh, 
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const uint2 w = hv ? __ldg(qrow + (h * D + (D / 4) * t + 4 * ks) / 4) : make_uint2(0u, 0u);
-      if (std::is_same<T, __half>::value) {
+      if (AS_IS || std::is_same<T, __half>::value) {
         qb[ks][nt][0] = w.x;
         qb[ks][nt][1] = w.y;
       } else {
@@ -1025,6 +1025,38 @@ __device__ __forceinline__ void load_q8(const Params& p, int s, int h0, int nh, 
       }
     }
   }
+}
+
+// The bf16 rows of a pair's heads, loaded as they are, become f16 times one power of two (q_lift, of
+// the largest finite value); returns its inverse.  One for all heads keeps it out of the scores'
+// arithmetic: they share their keys, so what f16 loses of a head's q, 2^-39 of the pair's largest,
+// moves its scores by 2^-39 of what the largest head's can reach.
+template <int KS, int NTH>
+__device__ __forceinline__ float lift_q8(uint32_t (&qb)[KS][NTH][2]) {
+  auto largest = [&](bool finite) -> uint32_t {
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = qb[ks][nt][i] & 0x7fff7fffu;
+          m2 = __vmaxu2(m2, finite ? w & __vcmpltu2(w, 0x7f807f80u) : w);
+        }
+    return __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+  };
+  uint32_t top = largest(false);
+  if (top >= 0x7f80u) top = largest(true);
+  const int fe = q_lift(top);
+  const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) qb[ks][nt][i] = q_lifted(qb[ks][nt][i], f);
+  return __uint_as_float(static_cast<uint32_t>(254 - fe) << 23);
 }
 
 // Q^T for INT4 blocks, as f16, in the d order the K fragments use: k-steps 2j and 2j + 1
@@ -1092,6 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
   constexpr bool FB = KV == kKvFp8Block;
   constexpr bool I4 = KV == kKvInt4;
   constexpr bool QK = KV != kKv16;  // quantised blocks
+  constexpr bool LIFT = FB && std::is_same<T, __nv_bfloat16>::value;  // q times a power of two
   using G_ = Geo<D, KV>;
   using TM = typename std::conditional<QK, __half, T>::type;  // MMA operand type
   constexpr int R = G_::kSlots;
@@ -1430,7 +1463,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     if (have) {
       const PairHeads ph = pair_heads(p, qf.g * p.gs + pi);
       if (I4) load_q4<D, NTH, T>(p, qf.s, ph.h0, ph.nh, lane, qn);
-      else if (F8) load_q8<D, NTH, T>(p, qf.s, ph.h0, ph.nh, lane, qn);
+      else if (F8) load_q8<D, NTH, T, LIFT>(p, qf.s, ph.h0, ph.nh, lane, qn);
       else load_q<D, NTH>(p, qf.s, ph.h0, ph.nh, lane, qn);
     }
   }
@@ -1478,9 +1511,14 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
       if (next_busy_fam(f, pi, phase, narrow, w0, w1, p, qf)) {
         const PairHeads lh = pair_heads(p, qf.g * p.gs + pi);
         if (I4) load_q4<D, NTH, T>(p, qf.s, lh.h0, lh.nh, lane, qn);
-        else if (F8) load_q8<D, NTH, T>(p, qf.s, lh.h0, lh.nh, lane, qn);
+        else if (F8) load_q8<D, NTH, T, LIFT>(p, qf.s, lh.h0, lh.nh, lane, qn);
         else load_q<D, NTH>(p, qf.s, lh.h0, lh.nh, lane, qn);
       }
+    }
+    // FB: the factor of a raw score and its K scale
+    float score_log2 = p.scale_log2;
+    if constexpr (LIFT) {
+      if (computes) score_log2 *= lift_q8<KS, NTH>(qb);
     }
 
     // INT4: each score starts from -(1032 Q_lo + 72 Q_hi) of its head, from the f16 q
@@ -1710,14 +1748,14 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
         float alpha[NTH][2];
 #pragma unroll
         for (int nt = 0; nt < NTH; ++nt) {
-          // FB: the K scale (with the softmax scale) of the tokens 16u + 8 hr .. + 7
+          // FB: the K scale (with the score's factor) of the tokens 16u + 8 hr .. + 7
           float bks[U][2];
           if constexpr (FB) {
             const float4 sk = *reinterpret_cast<const float4*>(&sm.bscale[warp][slot][0]);
-            bks[0][0] = sk.x * p.scale_log2;
-            bks[0][1] = sk.y * p.scale_log2;
-            bks[U - 1][0] = sk.z * p.scale_log2;
-            bks[U - 1][1] = sk.w * p.scale_log2;
+            bks[0][0] = sk.x * score_log2;
+            bks[0][1] = sk.y * score_log2;
+            bks[U - 1][0] = sk.z * score_log2;
+            bks[U - 1][1] = sk.w * score_log2;
           }
           float x[U][4];
 #pragma unroll

@@ -339,9 +339,8 @@ __device__ __forceinline__ uint32_t ld_early(const void* src) {
   return v;
 }
 
-// A bf16 row of q in shared memory (row r of a 128-row tile) becomes f16 values times 2^a, a
-// chosen so that the largest magnitude lies in [2^14, 2^15); returns 2^-a.  A row that holds
-// something not finite keeps a = 0.
+// A bf16 row of q in shared memory (row r of a 128-row tile) becomes f16 values times a power of
+// two (q_lift); returns its inverse.
 template <int D>
 __device__ __forceinline__ float q_row_to_f16(uint32_t tile, int r) {
   constexpr int CH = D / 8;
@@ -354,19 +353,13 @@ __device__ __forceinline__ float q_row_to_f16(uint32_t tile, int r) {
     m2 = __vmaxu2(m2, w.z & 0x7fff7fffu);
     m2 = __vmaxu2(m2, w.w & 0x7fff7fffu);
   }
-  const int e = static_cast<int>(max(m2 & 0xffffu, m2 >> 16) >> 7);  // exponent field, bias 127
-  const int fe = e == 255 ? 127 : min(253, 127 + 14 - (e - 127));
+  const int fe = q_lift(max(m2 & 0xffffu, m2 >> 16));
   const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
-  const float2 f2 = make_float2(f, f);
-  auto two = [&](uint32_t w) {
-    const float2 x = __fmul2_rn(unpack2<__nv_bfloat16>(w), f2);
-    return pack2<__half>(x.x, x.y);
-  };
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const uint32_t at = tile + swz(kRows, r, c);
     const uint4 w = ld_shared16(at);
-    st_shared16(at, make_uint4(two(w.x), two(w.y), two(w.z), two(w.w)));
+    st_shared16(at, make_uint4(q_lifted(w.x, f), q_lifted(w.y, f), q_lifted(w.z, f), q_lifted(w.w, f)));
   }
   return __uint_as_float(static_cast<uint32_t>(254 - fe) << 23);
 }

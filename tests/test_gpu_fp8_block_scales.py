@@ -257,3 +257,43 @@ def test_decode_of_values_whose_sum_passes_fp32(hq, hkv, ctx):
     caches = b.written()
     got, q, qs = decode(b, caches, q_bits, 0.125)
     check(b, caches, got, q, qs, 0.125)
+
+
+# ------------------------------------------------------------------------------ queries
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 128), (4, 1, 64), (32, 2, 128)])
+@pytest.mark.parametrize("ctx", [60, 2000])
+@pytest.mark.parametrize("up", [-90, -30, -13, 17, 60])
+def test_queries_of_any_size(hq, hkv, d, ctx, up):
+    """bf16 queries 2^up times as large over keys 2^-up times as large have the same scores, to the
+    bit, in decode and in prefill; each row has a power of two of its own, and a row of zeros."""
+    b = Batch([ctx, 90], hq, hkv, d, 16, "bf16", seed=11)
+    plain = b.written()
+    q = decode_bits(rows16(b.rng, (2, hq, d), "bf16", spread=3), "bf16")
+    q[1, 0] = 0.0
+    scale, outs = 1.0 / np.sqrt(d), []
+    for e in (0, up):
+        caches = [x.copy() for x in plain]
+        caches[2] = np.ldexp(caches[2], -e).astype(np.float32)
+        q_bits = encode_bits(np.ldexp(q, e), "bf16")
+        got, qf, qs = decode(b, caches, q_bits, scale)
+        check(b, caches, got, qf, qs, scale)
+        again, _, _ = prefill(b, caches, q_bits, [1, 1], scale)
+        check(b, caches, again, qf, qs, scale)
+        outs.append((got, again))
+    np.testing.assert_array_equal(outs[0][0], outs[1][0])
+    np.testing.assert_array_equal(outs[0][1], outs[1][1])
+
+
+def test_a_query_that_is_not_finite_reaches_its_head_and_no_other():
+    b = Batch([100, 2000], 8, 2, 128, 16, "bf16", seed=12)
+    caches = b.written()
+    q_bits = rows16(b.rng, (2, 8, 128), "bf16")
+    plain = pa.decode_fp8_block(dev16(q_bits, "bf16"), *upload(caches), dev(b.tables), dev(b.ctx), 0.1)
+    for what in (0x7F80, 0xFF80, 0x7FC0):
+        odd = q_bits.copy()
+        odd[:, 5, 77] = what
+        out = pa.decode_fp8_block(dev16(odd, "bf16"), *upload(caches), dev(b.tables), dev(b.ctx), 0.1)
+        assert torch.isnan(out[:, 5]).all()
+        keep = [0, 1, 2, 3, 4, 6, 7]
+        assert torch.equal(out[:, keep], plain[:, keep]) and device_error() == 0
