@@ -659,17 +659,6 @@ __device__ bool merge_pieces_group(const Params& p, int pi, const CutPiece& cp, 
   return true;
 }
 
-// Wait for the phase of `bar` with parity `parity`, bounded by kWaitLimitNs.
-__device__ __forceinline__ bool mbar_wait_limit(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
-  }
-}
-
-
 // merge_staged when every piece of both pairs fits in the ring at once: every piece's O
 // by one bulk copy, the (m, l) by plain loads behind them, a single round trip.
 template <int D, typename T, int KV>

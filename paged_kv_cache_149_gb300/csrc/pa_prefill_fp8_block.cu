@@ -43,7 +43,8 @@
 //   P <= 2^15 fits f16, whose smallest values only gain from it; the final O / l uses the same.
 //   (A limit of 8: 285 us, 15: 270 us for 8 prompts of 2048 tokens whose blocks' scales spread
 //   over 2^4, before V's scales went into the weights.)
-// Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag.
+// Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag; after one that gave up
+// each role still waits, as long again at most, for its own copies and MMAs in flight.
 //
 // What bounds it: the softmax's step of 64 keys, about 1710 cycles against 1024 of tensor work,
 // at 1240 instructions a step on each of an SM's schedulers (mostly exponentials, maxima, sums
@@ -619,7 +620,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       // softmax's step.)
       const int grp = lane & 7, quad = lane >> 3;
       const bool first_group = ((8 * grp) & (p.block_size - 1)) == 0;  // of its block
-      uint32_t num = 0, claims = 0, loads = 0;  // key tiles, claims and q loads so far
+      uint32_t num = 0, claims = 0, asked = 0, loads[kTiles] = {};  // key tiles, claims and q loads so far
+      auto claim = [&]() {
+        ++asked;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
+          claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
+        }
+      };
       Item it;
       if (!is_v) it = item_of(blockIdx.x);
       bool ok = true;
@@ -644,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             // contiguous in q) by TMA, one copy per 64-column half; a tile that runs past its
             // sequence by 16-byte copies, rows past the last token zeros.
             for (int t = 0; t < kTiles; ++t) {
-              if (loads > 0 && !(ok = wwait(sm.q_free[t], (loads - 1) & 1))) break;
+              if (loads[t] > 0 && !(ok = wwait(sm.q_free[t], (loads[t] - 1) & 1))) break;
+              ++loads[t];
               const int first = it.tok0 + t * tpt;
               const bool tma = p.q_tma && first + tpt <= it.end;
               if (lane == 0) {
@@ -671,7 +680,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
               cp_async_arrive(smem_addr(&sm.q_full[t]));
             }
             if (!ok) break;
-            ++loads;
           }
         }
         const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
@@ -712,10 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           for (int q = 0; q < 4 && base + q < n; ++q, ++num) {
             // the next item is claimed three tiles before this one's end: late, so that no SM
             // sits on work that another could start, yet early enough for the answer
-            if (!is_v && base + q == max(0, n - 3) && lane == 0) {
-              mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
-              claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
-            }
+            if (!is_v && base + q == max(0, n - 3)) claim();
             const bool mine_now = quad == q && first_group && e >= 0;  // (e < 0 past the groups)
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine_now)) * p.block_size * D;
             const int b = num & 1;
@@ -735,10 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         }
         if (!ok) break;
         if (!is_v) {
-          if (n == 0 && lane == 0) {
-            mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
-            claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
-          }
+          if (n == 0) claim();
           if (!(ok = wwait(sm.claim_full, claims & 1))) break;
           ++claims;
           const int x = claim_answer(smem_addr(&sm.claim));
@@ -748,6 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok) {
+        // after a wait that gave up: what this warp has in flight lands before the CTA ends
+        for (uint32_t b = 0; b < 2; ++b)
+          if (num > b) mbar_wait_limit(smem_addr(&sm.raw_full[is_v][b]), (num - 1 - b) >> 1 & 1);
+        for (int t = 0; t < kTiles; ++t)
+          if (loads[t] > 0) mbar_wait_limit(smem_addr(&sm.q_full[t]), (loads[t] - 1) & 1);
+        if (asked > claims) mbar_wait_limit(smem_addr(&sm.claim_full), claims & 1);
+      }
     } else {
       // ============ MMA issue: a warp per query tile ============
       // The tensor pipe runs one thread's MMAs in order, so S of a key tile may overwrite the P
@@ -825,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         rk = rv;
       }
       commit_el(smem_addr(&sm.fin[t]), el);  // every MMA this warp issued
-      wwait(sm.fin[t], 0);
+      if (!mbar_wait_limit(smem_addr(&sm.fin[t]), 0)) atomicOr(p.err, kErrTimeout);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
