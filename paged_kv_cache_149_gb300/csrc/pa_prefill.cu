@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     int ahead[kTableAhead];
 #pragma unroll
     for (int i = 0; i < kTableAhead; ++i) ahead[i] = lookup(i);
-    for (int kt = 0; kt < n; ++kt) {
+    int kt = 0;
+    for (; kt < n; ++kt) {
       const int st = kt % kStages;
       // this tile's blocks (lane j: block j), and the lookup kTableAhead tiles on
       const int my_e = ahead[0];
@@ -305,6 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       cp_async_arrive(smem_addr(&sm.kv_full[st]));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (kt < n) {
+      // after a wait that gave up: the copies in flight land before the rings are used otherwise
+      // (a stage that the other loader no longer fills runs into the limit)
+      for (int i = max(0, kt - kStages); i < kt; ++i)
+        mbar_wait_limit(smem_addr(&sm.kv_full[i % kStages]), (i / kStages) & 1);
+      if (!is_v) mbar_wait_limit(smem_addr(&sm.q_full), 0);
+    }
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ============ MMA issue: one thread per query tile (issue cost is per thread) ============
     if (lane == 0) {
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (ok) mma_commit(smem_addr(&sm.o_done[t][kt % kStages]));
       }
       mma_commit(smem_addr(&sm.fin));  // every MMA this thread issued
-      wait(sm.fin, 0);
+      if (!mbar_wait_limit(smem_addr(&sm.fin), 0)) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
   } else {
