@@ -297,3 +297,36 @@ def test_a_query_that_is_not_finite_reaches_its_head_and_no_other():
         assert torch.isnan(out[:, 5]).all()
         keep = [0, 1, 2, 3, 4, 6, 7]
         assert torch.equal(out[:, keep], plain[:, keep]) and device_error() == 0
+
+
+# ------------------------------------------------------------------------------ one rounding
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("B", [8, 16, 32])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 128), (8, 2, 64), (7, 1, 128), (12, 4, 128), (16, 1, 64), (64, 1, 128)])
+def test_weights_are_rounded_once_to_f16_whatever_the_outputs_type(dtype, B, hq, hkv, d):
+    """Ordinary batches: prompts from scratch, chunks and single tokens around the tiles and blocks."""
+    ctx, new = [1, B, 63, 64, 65, 129, 200, 333], [1, B, 5, 64, 65, 129, 77, 1]
+    b = Batch(ctx, hq, hkv, d, B, dtype, seed=hq * B + 1, spread=2)
+    caches, scale = b.written(), 1.0 / np.sqrt(d)
+    q_bits = rows16(b.rng, (sum(new), hq, d), dtype)
+    got, q, qs = prefill(b, caches, q_bits, new, scale)
+    check(b, caches, got, q, qs, scale, rows=(0, 1, 32, 76, 128))
+    got, q, qs = decode(b, caches, q_bits[:len(ctx)], scale)
+    check(b, caches, got, q, qs, scale)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("B,hq,hkv,d", [(8, 4, 2, 64), (16, 8, 2, 128), (32, 16, 1, 128)])
+def test_scales_that_are_no_powers_of_two(dtype, B, hq, hkv, d):
+    """A cache made elsewhere, over a range of 2^12: codes are exact whatever the scale is."""
+    b = Batch([300, 77], hq, hkv, d, B, dtype, seed=B)
+    caches = [x.copy() for x in b.written()]
+    for c in caches[2:]:
+        c *= np.exp2(b.rng.uniform(-6, 6, c.shape)).astype(np.float32)
+    caches[2] *= np.float32(2.0 ** -4)
+    q_bits, scale = rows16(b.rng, (277, hq, d), dtype), 1.0 / np.sqrt(d)
+    got, q, qs = prefill(b, caches, q_bits, [200, 77], scale)
+    check(b, caches, got, q, qs, scale, rows=(0, 17, 76, 150, 199), odd=True)
+    got, q, qs = decode(b, caches, q_bits[:2], scale)
+    check(b, caches, got, q, qs, scale, odd=True)
