@@ -44,7 +44,7 @@
 //   (A limit of 8: 285 us, 15: 270 us for 8 prompts of 2048 tokens whose blocks' scales spread
 //   over 2^4, before V's scales went into the weights.)
 // Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag; after one that gave up
-// each role still waits, as long again at most, for its own copies and MMAs in flight.
+// the CTA still waits, as long again at most, for its copies and MMAs in flight.
 //
 // What bounds it: the softmax's step of 64 keys, about 1710 cycles against 1024 of tensor work,
 // at 1240 instructions a step on each of an SM's schedulers (mostly exponentials, maxima, sums
@@ -196,6 +196,9 @@ struct Smem {
   unsigned long long fin[kTiles];              // an MMA warp's last commit
   uint32_t tmem;
   int abort;  // a wait gave up: every role stops
+  // copies asked for so far (of an aborted CTA the last ones may be in flight): tiles of raw codes,
+  // q tiles, claims
+  uint32_t raw_sent[2], q_sent[kTiles], claim_sent;
 };
 
 #define PA_R4(a) "=r"(r[a]), "=r"(r[a + 1]), "=r"(r[a + 2]), "=r"(r[a + 3])
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
     }
     fence_mbar_init();
     sm.abort = 0;
+    sm.raw_sent[0] = sm.raw_sent[1] = sm.q_sent[0] = sm.q_sent[1] = sm.claim_sent = 0;
   }
   if (warp == kMmaWarp + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -620,14 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
       // softmax's step.)
       const int grp = lane & 7, quad = lane >> 3;
       const bool first_group = ((8 * grp) & (p.block_size - 1)) == 0;  // of its block
-      uint32_t num = 0, claims = 0, asked = 0, loads[kTiles] = {};  // key tiles, claims and q loads so far
-      auto claim = [&]() {
-        ++asked;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
-          claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
-        }
-      };
+      uint32_t num = 0, claims = 0, loads = 0;  // key tiles, claims and q loads so far
       Item it;
       if (!is_v) it = item_of(blockIdx.x);
       bool ok = true;
@@ -652,11 +649,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             // contiguous in q) by TMA, one copy per 64-column half; a tile that runs past its
             // sequence by 16-byte copies, rows past the last token zeros.
             for (int t = 0; t < kTiles; ++t) {
-              if (loads[t] > 0 && !(ok = wwait(sm.q_free[t], (loads[t] - 1) & 1))) break;
-              ++loads[t];
+              if (loads > 0 && !(ok = wwait(sm.q_free[t], (loads - 1) & 1))) break;
               const int first = it.tok0 + t * tpt;
               const bool tma = p.q_tma && first + tpt <= it.end;
               if (lane == 0) {
+                sm.q_sent[t] = loads + 1;
                 mbar_arrive_expect_tx(smem_addr(&sm.q_full[t]), tma ? kRows * D * 2 : 0);
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
@@ -680,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
               cp_async_arrive(smem_addr(&sm.q_full[t]));
             }
             if (!ok) break;
+            ++loads;
           }
         }
         const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
@@ -720,7 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           for (int q = 0; q < 4 && base + q < n; ++q, ++num) {
             // the next item is claimed three tiles before this one's end: late, so that no SM
             // sits on work that another could start, yet early enough for the answer
-            if (!is_v && base + q == max(0, n - 3)) claim();
+            if (!is_v && base + q == max(0, n - 3) && lane == 0) {
+              sm.claim_sent = claims + 1;
+              mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
+              claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
+            }
             const bool mine_now = quad == q && first_group && e >= 0;  // (e < 0 past the groups)
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine_now)) * p.block_size * D;
             const int b = num & 1;
@@ -730,7 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             if (quad == q && !is_v && grp % (8 / NG) == 0)
               sm.factor[num % kFactorSlots][grp / (8 / NG)] = make_float2(kf, vl);
             __syncwarp();  // the stores above before the arrival
-            if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]), bytes);
+            if (lane == 0) {
+              sm.raw_sent[is_v] = num + 1;
+              mbar_arrive_expect_tx(smem_addr(&sm.raw_full[is_v][b]), bytes);
+            }
             __syncwarp();
             if (mine_now)
               tma_load_4d(smem_addr(sm.raw[is_v][b]) + 8 * grp * D, is_v ? &p.vmap : &p.kmap, 0, 0, it.g, e,
@@ -740,7 +745,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         }
         if (!ok) break;
         if (!is_v) {
-          if (n == 0) claim();
+          if (n == 0 && lane == 0) {
+            sm.claim_sent = claims + 1;
+            mbar_arrive_expect_tx(smem_addr(&sm.claim_full), 16);
+            claim_ask(smem_addr(&sm.claim), smem_addr(&sm.claim_full));
+          }
           if (!(ok = wwait(sm.claim_full, claims & 1))) break;
           ++claims;
           const int x = claim_answer(smem_addr(&sm.claim));
@@ -750,14 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!ok) {
-        // after a wait that gave up: what this warp has in flight lands before the CTA ends
-        for (uint32_t b = 0; b < 2; ++b)
-          if (num > b) mbar_wait_limit(smem_addr(&sm.raw_full[is_v][b]), (num - 1 - b) >> 1 & 1);
-        for (int t = 0; t < kTiles; ++t)
-          if (loads[t] > 0) mbar_wait_limit(smem_addr(&sm.q_full[t]), (loads[t] - 1) & 1);
-        if (asked > claims) mbar_wait_limit(smem_addr(&sm.claim_full), claims & 1);
-      }
     } else {
       // ============ MMA issue: a warp per query tile ============
       // The tensor pipe runs one thread's MMAs in order, so S of a key tile may overwrite the P
@@ -835,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
         rk = rv;
       }
       commit_el(smem_addr(&sm.fin[t]), el);  // every MMA this warp issued
-      if (!mbar_wait_limit(smem_addr(&sm.fin[t]), 0)) atomicOr(p.err, kErrTimeout);
+      wwait(sm.fin[t], 0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -1021,6 +1022,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
   }
   tc_fence_before();
   __syncthreads();
+  if (sm.abort) {
+    // what is in flight ends before the CTA leaves its memory (every role has stopped)
+    if (tid == 0) {
+      bool ended = true;
+      auto land = [&](unsigned long long& bar, uint32_t sent) {  // the last of `sent` phases
+        if (sent > 0) ended = mbar_wait_limit(smem_addr(&bar), (sent - 1) & 1) && ended;
+      };
+      for (int i = 0; i < 2; ++i)
+        for (uint32_t b = 0; b < 2; ++b) land(sm.raw_full[i][b], (sm.raw_sent[i] + 1 - b) / 2);
+      for (int t = 0; t < kTiles; ++t) land(sm.q_full[t], sm.q_sent[t]), land(sm.fin[t], 1);
+      land(sm.claim_full, sm.claim_sent);
+      if (!ended) atomicOr(p.err, kErrTimeout);
+    }
+    __syncthreads();
+  }
   if (warp == kMmaWarp + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
