@@ -1144,9 +1144,10 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
 
   // The next kernel in the stream may start launching.  Everything up to the first copy
   // reads only context_lens and block_tables (the share, the first family, the first
-  // stages' table entries), which no kernel of this library writes; it runs while the
-  // kernel before this one drains.  The wait comes before anything touches q, the caches
-  // or the workspace.
+  // stages' table entries); it runs while the kernel before this one drains.  So a kernel
+  // that writes those must let no dependent start early: pa_build_step, the only one of this
+  // library that does, is launched plainly and has no early trigger.  The wait comes before
+  // anything touches q, the caches or the workspace.
   pdl_launch_dependents();
 
   if (lane == 0) {

@@ -336,10 +336,11 @@ __device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&v)[4])
                : "memory");
 }
 
-// A 32-bit load of data that no kernel of the call writes, kept at its place in the program.
+// A 32-bit load kept at its place in the program.  (Not by the non-coherent path: the kernel that
+// wrote the scales may have run beside this one's start.)
 __device__ __forceinline__ uint32_t ld_early(const void* src) {
   uint32_t v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(src));
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(src));
   return v;
 }
 
