@@ -244,6 +244,9 @@ int pa_swap_blocks_int4(const void* src_k, const void* src_v, const float* src_k
  *   slot_mapping[N_s + i] = block_tables[s][p / B] * B + p % B,          p = c_s - q_s + i
  *   query_start[s] = N_s,   query_start[num_seqs] = N,   free_next[0] = free_start[0] + sum need
  * Blocks leave the head of the list in request order, as from the host pool's free list.
+ * On top of the host pool the list is a reserve: the table of blocks that pa_pool_allocate gives an
+ * id of its own.  The pool counts them as that id's until pa_pool_free takes them all back, whichever
+ * requests hold them by then; fork, prefix caching and swap planning know the pool's ids alone.
  * slot_mapping entries N .. num_slots - 1 are -1 (a padded batch: the cache writes skip
  * them).  Other table entries are left as they were; the old_s entries of a request are read.
  * A request may have no new tokens (q_s = 0) and no context.  A tail block shared with
