@@ -1194,7 +1194,8 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     // are larger than that are cut as ever.  One sequence of 512 / 4096 / 16384 tokens, 8 kv
     // heads of 128, 4 query heads each: 12.9 / 22.6 / 36.1 us against 14.8 / 47.5 / 56.1 us
     // with shares of one step at least (and 31.1 / 38.3 us at 512 / 4096, head dim 64, with
-    // any); 8 sequences of 8-32 K tokens are cut as before.
+    // any); 8 sequences of 8-32 K tokens are cut as before.  (Measured, like the figures below,
+    // before the V scales went into the weights, which adds 3 to 5 % to such batches.)
     int longest = 0;
     for (int w = 0; w < kWarps; ++w) longest = max(longest, sm.longest[w]);
     const long long families = static_cast<long long>(p.num_seqs) * p.ngroups;

@@ -20,10 +20,12 @@
 // and nothing is shared between warps.  The tasks of a ragged batch are counted by a scan
 // over the sequences that every CTA makes for itself, and cut into equal shares, so one
 // long chunk among many single tokens keeps no SM waiting.  Measured on GB300, 13 ragged
-// prompts of 300..2048 tokens (94 MB, floor 13.9 us at the copy peak): 23.3 us at first; 21.4
-// with the next task's table lookup under this one's loads; 16.3 (85 % of the peak) with the
-// magnitudes compared as integers, a second look only where one is not finite, and registers
-// held to four CTAs an SM (three before).  One token each of 64 sequences: 3.4 us.
+// prompts of 300..2048 tokens (94 MB, floor 13.9 us at the copy peak), call after call on the same
+// buffers, which the L2 holds: 23.3 us at first; 21.4 with the next task's table lookup under this
+// one's loads; 16.3 with the magnitudes compared as integers, a second look only where one is not
+// finite, and registers held to four CTAs an SM (three before).  Over rotating buffers 19.0 us, 73 %
+// of the copy peak: a warp loads its rows, reduces and stores before it loads the next, so DRAM
+// waits (41 % busy, 60 % of the issue slots used).  One token each of 64 sequences: 3.4 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

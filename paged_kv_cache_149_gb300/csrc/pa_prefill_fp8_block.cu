@@ -46,12 +46,14 @@
 // Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag; after one that gave up
 // the CTA still waits, as long again at most, for its copies and MMAs in flight.
 //
-// What bounds it: the softmax's step of 64 keys, about 1710 cycles against 1024 of tensor work,
-// at 1240 instructions a step on each of an SM's schedulers (mostly exponentials, maxima, sums
-// and the widening); then 5300 to 9000 cycles from an item's last P to the next item's first.
-// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 272 us (1011
-// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 183 us (1022 TFLOP/s).  The 16-bit
-// prefill takes 292 and 202 us there.
+// What bounds it: the softmax's step of 64 keys, 1255 instructions on each of an SM's schedulers
+// (mostly exponentials, maxima, sums and the widening) and their latency, about 1710 cycles against
+// 1024 of tensor work when stamped (before V's scales went into the weights); then 5300 to 9000
+// cycles from an item's last P to the next item's first.
+// On GB300: 8 prompts of 2048 tokens, 32 query / 8 kv heads of 128, bf16, 275 us (1000
+// TFLOP/s); 16 chunks of 100..512 over 1024..3500, fp16, 185 us (1010 TFLOP/s).  The 16-bit
+// prefill takes 292 and 202 us there.  (With codes widened relative to the largest scale near
+// them, which let a block that a row does not attend to take its bits: 265 and 187 us.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1063,9 +1065,9 @@ int launch(const Params& prm, int max_query_len, int sm_count, cudaStream_t stre
   };
   long long count = items(kTiles);
   // Few items: one query tile each while every item still has an SM of its own.  One prompt
-  // of 128 / 512 tokens, 8 kv heads, 4 query heads each: 8.4 / 13.1 us, 10.0 / 15.0 us with
-  // two; a chunk of 512 over 2000 cached 34.7 us, 41.5 with two.  Past that, items queue: 8
-  // chunks of 100 over 1000 cached (128 items of two) 41.0 us, 25.0 with two.
+  // of 128 / 512 tokens, 8 kv heads, 4 query heads each: 8.3 / 14.1 us, 9.6 / 15.1 us with
+  // two; a chunk of 512 over 2000 cached 39.2 us, 45.1 with two.  Past that, items queue: 8
+  // chunks of 100 over 1000 cached (128 items of two) 42.1 us, 27.1 with two.
   if (2 * count <= sm_count) count = items(1);
   if (count > 0x7fffffffLL) return -1;
   cfg.gridDim = dim3(static_cast<unsigned>(count));
