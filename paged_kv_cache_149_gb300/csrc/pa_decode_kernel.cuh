@@ -1095,9 +1095,9 @@ __device__ __forceinline__ bool next_busy_fam(Fam f, int pi, int phase, int narr
 // straddle a block, so a stage has four groups of tokens with one K and one V scale each,
 // and a lane's scores of one (m-tile, half) lie in one group: the K scale is one factor of
 // each score z (log2).  The V scale goes into the weights that P V rounds to f16: 2^(z + log2 sV - r),
-// r each head's largest z + log2 sV so far, rounded up (with log2 sV whole, as the cache write's
-// powers of two are, the difference is exact).  So f16 rounds weights where they count in O, and
-// neither a scale nor a token without weight costs another token's bits.  The sum of the weights
+// r each head's largest z + log2 sV so far.  So f16 rounds weights where they count in O, the
+// largest, where one stands out, is 1 and not rounded, and neither a scale nor a token without weight
+// costs another token's bits.  The sum of the weights
 // themselves is each lane's own, against the largest score that the lane has met: it needs no
 // exchange until the pair's end.
 // KV = kKvInt4: K/V blocks hold INT4 codes with a float32 scale per row: a token's K scale
@@ -1773,7 +1773,7 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
               my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 4));
               my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 8));
               my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 16));
-              const float r_new = fmaxf(r_run[nt][cc], ceilf(my)), m_new = fmaxf(m_run[nt][cc], mx);
+              const float r_new = fmaxf(r_run[nt][cc], my), m_new = fmaxf(m_run[nt][cc], mx);
               alpha[nt][cc] = fast_exp2(r_run[nt][cc] - r_new);
               l_run[nt][cc] *= fast_exp2(m_run[nt][cc] - m_new);
 #pragma unroll

@@ -12,10 +12,10 @@
 // operands, so no scale, of a key that a row attends to or of one that it does not, costs another
 // key's code a bit.  K's multiply the scores in the softmax, a factor per group of keys.  V's go
 // into the weights, 2^(z_t + log2 sV_t - r), r a reference of each row's own: the largest
-// z + log2 sV among the keys that it attends to (rounded up, moved when outgrown, with O), so that
-// f16 rounds weights where they count in O; the sum of weights takes the factor out again, group
-// by group.  (log2 sV is whole for the scales that the cache write stores.)  Each bf16 row of q is
-// multiplied by the power of two that brings its largest value to [2^14, 2^15).
+// z + log2 sV among the keys that it attends to (moved when outgrown, with O), so that f16 rounds
+// weights where they count in O; the sum of weights takes the factor out again, group by group.
+// Each bf16 row of q is multiplied by the power of two that brings its largest value to
+// [2^14, 2^15).
 //
 // Design: persistent CTAs of 640 threads, one per SM; a work item is a (pair of 128-row query
 // tiles, sequence, kv head).  The grid has a CTA per item; a running CTA claims items of CTAs
@@ -39,10 +39,10 @@
 //   ones, so each softmax finds its next scores ready.
 // * Two softmax warpgroups, one per query tile, one thread per row: the row's 64 scores in
 //   registers, mask, references m (of the scores) and r (of the scores with V's scale) and sum l in
-//   exp2 units, P.  O is rescaled only when a row outgrows r by more than 15 (log2) or m by 40, so
-//   P <= 2^15 fits f16, whose smallest values only gain from it; the final O / l uses the same.
-//   (A limit of 8: 285 us, 15: 270 us for 8 prompts of 2048 tokens whose blocks' scales spread
-//   over 2^4, before V's scales went into the weights.)
+//   exp2 units, P.  O is rescaled only when a row outgrows r by more than 15.9 (log2) or m by 40,
+//   so P < 2^16 fits f16, whose smallest values only gain from it; the final O / l uses the same.
+//   (A limit of 15: 280 us, 15.9: 277 us for 8 prompts of 2048 tokens whose blocks' scales spread
+//   over 2^4; 8: 15 us more than 15, before V's scales went into the weights.)
 // Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag; after one that gave up
 // the CTA still waits, as long again at most, for its copies and MMAs in flight.
 //
@@ -86,7 +86,7 @@ constexpr int kThreads = 32 * (kWidenWarp + 2 * kWidenWarps);
 constexpr int kSoftmaxRegs = 144;
 constexpr int kOtherRegs = 64;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescale = 15.f;     // log2 growth past a row's r that forces a rescale of O, P <= 2^15
+constexpr float kRescale = 15.9f;    // log2 growth past a row's r that forces a rescale of O: P < 2^16
 constexpr float kLag = 40.f;         // past its m: fp32 sums of weights up to 2^40
 // Weights of groups with far smaller V scales than the row's largest are held up to 2^(z - m - kDeep),
 // at most 2^-40: zero in f16 P as they would be, and they still count in l.
@@ -900,10 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
           mx = fmax3(mx, m[0], m[1]);
           my = fmax3(my, y[0], y[1]);
         }
-        // (whole references, so that they and whole log2 scales add exactly)
+        // (not rounded up: where one key stands out its weight is 1 then, which f16 does not round)
         if (kt == 0) {
-          m_ref = mx > -INFINITY ? ceilf(mx) : kLowest;
-          r_ref = my > -INFINITY ? ceilf(my) : kLowest;
+          m_ref = mx > -INFINITY ? mx : kLowest;
+          r_ref = my > -INFINITY ? my : kLowest;
         } else {
           const bool need = mx > m_ref + kLag || my > r_ref + kRescale;
           if (__any_sync(0xffffffffu, need)) {
@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_block_kernel(const __
             tc_fence_after();
             float alpha = 1.f;
             if (need) {
-              const float m_new = fmaxf(m_ref, ceilf(mx)), r_new = fmaxf(r_ref, ceilf(my));
+              const float m_new = fmaxf(m_ref, mx), r_new = fmaxf(r_ref, my);
               l_run *= ex2(m_ref - m_new);
               alpha = ex2(r_ref - r_new);
               m_ref = m_new;

@@ -48,6 +48,8 @@ def expected(q, k, v, sv, scale, dtype, odd=False):
         to f16's upper range, loses 2^-39 of its largest value at most), two fp32 factors, an
         exp2 off by 2^-22 and its argument's rounding: numerator and denominator;
       * n sums in fp32 and rescalings, n 2^-22;
+      * the base-2 logarithm of V's scale joins the exponent and leaves it again, two roundings in
+        fp32 of up to twice its size: 2^-22 of it;
       * weights times their block's scale that f16 holds as subnormals: 2^-25 each against the
         largest weighted scale rounded up to a power of two, W, times the code;
       * odd: scales that are no powers of two go through a base-2 logarithm of two units in
@@ -64,7 +66,7 @@ def expected(q, k, v, sv, scale, dtype, odd=False):
         delta = (abs(scale) * (d * 2.0 ** -22 * (np.abs(kh) @ np.abs(q[h]))
                                + 2.0 ** -39 * np.abs(q[h]).max() * np.abs(kh).sum(1))
                  + 2.0 ** -21 * np.abs(z) + 2.0 ** -22 * (z.max() - z) + 2.0 ** -21)
-        rel = 2.0 ** -11 + n * 2.0 ** -22 + (2.0 ** -16 if odd else 0)
+        rel = 2.0 ** -11 + (n + np.abs(np.log2(sh)).max()) * 2.0 ** -22 + (2.0 ** -16 if odd else 0)
         code = np.abs(vh) / sh[:, None]
         most[h] = ((rel * (w @ np.abs(vh)) + (w * delta) @ (np.abs(vh) + np.abs(out[h]))
                     + 2.0 ** -24 * (w * sh).max() * code.sum(0)) * (1 + HALF_STEP[dtype])
@@ -330,3 +332,31 @@ def test_scales_that_are_no_powers_of_two(dtype, B, hq, hkv, d):
     check(b, caches, got, q, qs, scale, rows=(0, 17, 76, 150, 199), odd=True)
     got, q, qs = decode(b, caches, q_bits[:2], scale)
     check(b, caches, got, q, qs, scale, odd=True)
+
+
+@pytest.mark.parametrize("ctx,at", [(30, 3), (100, 99), (700, 40), (700, 650)])
+def test_the_weight_of_a_key_that_stands_out_is_not_rounded(ctx, at):
+    """One key scores e^17 and more above the others, by another fraction in each sequence: its
+    weight is 1 within 2^-14, so an fp16 output is its value to half a step, whichever tile it is
+    in.  (Scales that are no powers of two, so that the values are no fp16 numbers; their base-2
+    logarithms are off by 2^-16.)"""
+    n, hq, hkv, d, B = 24, 8, 4, 128, 16
+    b = Batch([ctx] * n, hq, hkv, d, B, "fp16", seed=ctx + at)
+    q_row = b.rng.choice([-1.0, 1.0], d) * 0.25
+    b.key[:] = encode_bits(decode_bits(b.key, "fp16") * 2.0 ** -6, "fp16")
+    for s in range(n):
+        b.key[int(b.qs[s]) + at] = encode_bits(np.broadcast_to((18 + s / 24) * q_row / (q_row @ q_row), (hkv, d)), "fp16")
+    caches = [x.copy() for x in b.written()]
+    caches[3] *= b.rng.uniform(1, 2, caches[3].shape).astype(np.float32)
+    q_bits = encode_bits(np.broadcast_to(q_row, (n, hq, d)).copy(), "fp16")
+    got, q, qs = decode(b, caches, q_bits, 1.0)
+    again, _, _ = prefill(b, caches, q_bits, [1] * n, 1.0)
+    for s in range(n):
+        k, v, _ = rows_of(b, caches, s, ctx)
+        top = v[at].repeat(hq // hkv, 0)
+        z = np.stack([k[:, h // 2] @ q[s, h] for h in range(hq)], 1)
+        rest = np.delete(np.exp(z - z.max(0)), at, 0).sum(0)[:, None]
+        assert (rest < 2.0 ** -14).all()
+        half = np.spacing(np.abs(top).astype(np.float16)).astype(np.float64) / 2
+        most = half * (1 + 2.0 ** -10) + 2.0 ** -16 * np.abs(top) + (rest + 2.0 ** -20) * 2 * np.abs(v).max()
+        assert (np.abs(got[s] - top) <= most).all() and (np.abs(again[s] - top) <= most).all(), s
