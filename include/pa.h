@@ -330,7 +330,8 @@ int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
 /* pa_prefill over those blocks: the arguments and rules of pa_prefill with K and V the values
  * decode(code) * scale of each token's block, and two more: num_tokens, the rows of q and out
  * (a sequence whose span lies outside them gets PA_DEVERR_BAD_CONTEXT and nothing is read
- * or written for it; rows behind the last sequence are not touched), and scale > 0.
+ * or written for it; rows behind the last sequence are not touched), and scale > 0;
+ * num_q_heads <= 65536.
  * Products run in f16 over the codes, widened exactly, and bf16 rows of q brought to the type's
  * upper range by a power of two; K's scales multiply the fp32 scores, V's the softmax weights before
  * they are rounded to f16, relative to the largest such product of the keys that the token attends

@@ -535,7 +535,8 @@ int pa_prefill_fp8_block(const void* q, const void* k_cache, const void* v_cache
                          int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
                          int head_dim, int block_size, int num_blocks, float scale, void* out,
                          pa_dtype dtype, cudaStream_t stream) {
-  if (num_tokens < 0 || !(scale > 0.f)) return PA_ERR_ARG;
+  // (the kernel's offsets of a query tile's rows within out are 32-bit)
+  if (num_tokens < 0 || !(scale > 0.f) || num_q_heads > 65536) return PA_ERR_ARG;
   if (num_tokens < max_query_len) max_query_len = num_tokens;  // (no sequence has more rows)
   if (num_seqs > 0 && max_query_len > 0 &&
       !fp8_block_arrays_ok(k_cache, v_cache, k_scales, v_scales))
