@@ -710,9 +710,11 @@ class _Torch:
         self.i32, self.i64, self.f32, self.u8 = torch.int32, torch.int64, torch.float32, torch.uint8
         self.f8, self.f16, self.bf16 = torch.float8_e4m3fn, torch.float16, torch.bfloat16
         self.module, self.empty_like, self.device = torch, torch.empty_like, torch.cuda.device
-        # (None in a torch without CUDA, whose tensors no call gets as far with)
-        self.current_device = getattr(torch._C, "_cuda_getDevice", None)
-        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # torch's private shortcuts, which spare a call its checks; the public calls where a torch
+        # has none of them
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 _T = None
