@@ -1976,9 +1976,10 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
     }
     const bool whole = r.x == 0 && r.y == f.ns;
     if constexpr (FB) {
-      // The column's m and l from its lanes', and O against m in r's place.  m is made whole, and O
-      // and l are taken down together (m up) by a power of two that leaves l in [2^-9, 2^-8), so that
-      // O stays a float where the values are near its end: also the sum of 256 pieces.
+      // The column's m (whole) and l from its lanes', and O against m in r's place.  Where that makes
+      // O larger, it and l are taken down together (m up) by a power of two that leaves l in
+      // [2^-13, 2^-12): with values near a float's end O stays one, and so does the sum over eight
+      // warps of each of 512 CTAs.
 #pragma unroll
       for (int nt = 0; nt < NTH; ++nt)
 #pragma unroll
@@ -1992,18 +1993,16 @@ __global__ void __launch_bounds__(kThreads, 1) PA_DECODE_KERNEL(const __grid_con
           l += __shfl_xor_sync(0xffffffffu, l, 8);
           l += __shfl_xor_sync(0xffffffffu, l, 16);
           const bool none = m <= kLowest;  // no units, or no score that is a number
-          const int down = none ? 0 : min(static_cast<int>(__float_as_uint(l) >> 23) - 127 + 9, 60);
-          const float fd = __uint_as_float(static_cast<uint32_t>(127 - down) << 23);
           const float d = r_run[nt][cc] - m;
-          // (2^d and 2^-down apart where d is low, as their product may be no float)
-          const float f = none ? 1.f : exp2f(d > 0.f ? d - down : d), g = d > 0.f ? 1.f : fd;
+          const int down = none || d <= 0.f ? 0 : min(static_cast<int>(__float_as_uint(l) >> 23) - 127 + 13, 60);
+          const float f = none ? 1.f : exp2f(d - down);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            o[mt][nt][cc] = o[mt][nt][cc] * f * g;
-            o[mt][nt][cc + 2] = o[mt][nt][cc + 2] * f * g;
+            o[mt][nt][cc] *= f;
+            o[mt][nt][cc + 2] *= f;
           }
           m_run[nt][cc] = none ? -INFINITY : m + down;
-          l_run[nt][cc] = l * fd;
+          l_run[nt][cc] = l * __uint_as_float(static_cast<uint32_t>(127 - down) << 23);
         }
     }
     const int slot_out = cta_first ? 0 : 1;

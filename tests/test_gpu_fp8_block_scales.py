@@ -261,6 +261,21 @@ def test_decode_of_values_whose_sum_passes_fp32(hq, hkv, ctx):
     check(b, caches, got, q, qs, 0.125)
 
 
+def test_decode_of_one_long_sequence_of_the_largest_values():
+    """300000 values of 2^127 in every warp of every SM: their average is 2^127."""
+    ctx, B, d = 300000, 16, 64
+    gen, nb = torch.Generator(device="cuda").manual_seed(1), 300000 // 16
+    k8 = torch.randint(0, 0x50, (nb, 1, B, d), generator=gen, device="cuda", dtype=torch.uint8)  # up to 12
+    v8 = torch.full_like(k8, 0x70)  # 128
+    ks, vs = torch.full((nb, 1), 0.125, device="cuda"), torch.full((nb, 1), 2.0 ** 120, device="cuda")
+    q = torch.randn(1, 1, d, generator=gen, device="cuda").bfloat16()
+    out = pa.decode_fp8_block(q, k8, v8, ks, vs, torch.arange(nb, dtype=torch.int32, device="cuda")[None],
+                              dev([ctx], np.int32), 0.125)
+    # weights rounded to f16 (2^-11) over unrounded sums, and 2^-22 for each of the sums
+    most = 2.0 ** 127 * (2.0 ** -11 + ctx * 2.0 ** -22 + HALF_STEP["bf16"])
+    assert device_error() == 0 and np.abs(values(out, "bf16") - 2.0 ** 127).max() <= most
+
+
 # ------------------------------------------------------------------------------ queries
 
 @pytest.mark.parametrize("hq,hkv,d", [(8, 8, 128), (4, 1, 64), (32, 2, 128)])
