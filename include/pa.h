@@ -315,10 +315,11 @@ int pa_append_fp8_block(const void* key, const void* value, void* k_cache, void*
  * softmax(z)_t * sV_t * decode(V codes_t), sK_t and sV_t the scales of token t's block.  q and
  * out are fp16 or bf16 (`dtype`).  The codes are widened to f16 exactly and multiplied on the
  * tensor cores in f16; bf16 queries, those of a kv head together, are brought to the type's upper
- * range by a power of two, so that queries of any size keep their bits.  The K scale multiplies
- * the fp32 scores, the V scale the softmax weights before they are rounded to f16, relative to
- * the largest product of a weight and its V scale: f16 loses 2^-25 of that at most, so a block
- * of large values with next to no weight costs the others no precision.  Accumulation fp32;
+ * range by a power of two, so that queries of any size can be used: f16 loses 2^-39 of the
+ * largest of them at most.  The K scale multiplies the fp32 scores, the V scale the softmax
+ * weights before they are rounded to f16, relative to the largest product of a weight and its V
+ * scale: f16 loses 2^-25 of that at most, so a block of large values with next to no weight
+ * costs the others no precision.  Accumulation fp32;
  * outputs past the type's largest value are clamped to it (a cached 65504 is held as 65536).
  * Same workspace, ordering, error and determinism rules as pa_decode. */
 int pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,

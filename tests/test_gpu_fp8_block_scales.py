@@ -44,9 +44,10 @@ def expected(q, k, v, sv, scale, dtype, odd=False):
       * the output's own rounding, half a step;
       * weights rounded once to f16 before P V, 2^-11 of sum w |v|;
       * a weight off by delta_t because its score is: d exact products summed in fp32 (tensor cores
-        add with at least 2^-22 relative to the terms' magnitudes each; a bf16 row of q, brought
-        to f16's upper range, loses 2^-39 of its largest value at most), two fp32 factors, an
-        exp2 off by 2^-22 and its argument's rounding: numerator and denominator;
+        add with at least 2^-22 relative to the terms' magnitudes each; bf16 rows of q, brought to
+        f16's upper range, those of a kv head together in decode, lose 2^-39 of their largest
+        value at most), two fp32 factors, an exp2 off by 2^-22 and its argument's rounding:
+        numerator and denominator;
       * n sums in fp32 and rescalings, n 2^-22;
       * the base-2 logarithm of V's scale joins the exponent and leaves it again, two roundings in
         fp32 of up to twice its size: 2^-22 of it;
@@ -64,7 +65,7 @@ def expected(q, k, v, sv, scale, dtype, odd=False):
         w /= w.sum()
         out[h] = w @ vh
         delta = (abs(scale) * (d * 2.0 ** -22 * (np.abs(kh) @ np.abs(q[h]))
-                               + 2.0 ** -39 * np.abs(q[h]).max() * np.abs(kh).sum(1))
+                               + 2.0 ** -39 * np.abs(q.reshape(hkv, -1)[g]).max() * np.abs(kh).sum(1))
                  + 2.0 ** -21 * np.abs(z) + 2.0 ** -22 * (z.max() - z) + 2.0 ** -21)
         rel = 2.0 ** -11 + (n + np.abs(np.log2(sh)).max()) * 2.0 ** -22 + (2.0 ** -16 if odd else 0)
         code = np.abs(vh) / sh[:, None]
@@ -300,6 +301,21 @@ def test_queries_of_any_size(hq, hkv, d, ctx, up):
         outs.append((got, again))
     np.testing.assert_array_equal(outs[0][0], outs[1][0])
     np.testing.assert_array_equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (32, 2, 64), (20, 1, 128)])
+def test_queries_of_different_sizes_in_a_group(hq, hkv, d):
+    """Heads of one kv head whose queries lie up to 2^24 apart."""
+    b = Batch([70, 900], hq, hkv, d, 16, "bf16", seed=13)
+    caches = b.written()
+    q = decode_bits(rows16(b.rng, (2, hq, d), "bf16"), "bf16")
+    q = np.ldexp(q, np.linspace(-20, 4, hq).round().astype(int)[None, :, None])
+    for order in (slice(None), slice(None, None, -1)):
+        q_bits = encode_bits(np.ascontiguousarray(q[:, order]), "bf16")
+        got, qf, qs = decode(b, caches, q_bits, 1.0 / np.sqrt(d))
+        check(b, caches, got, qf, qs, 1.0 / np.sqrt(d))
+        got, qf, qs = prefill(b, caches, q_bits, [1, 1], 1.0 / np.sqrt(d))
+        check(b, caches, got, qf, qs, 1.0 / np.sqrt(d))
 
 
 def test_a_query_that_is_not_finite_reaches_its_head_and_no_other():
