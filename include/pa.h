@@ -49,8 +49,9 @@ extern "C" {
 
 /* PA_FP8_E4M3 names FP8 K/V blocks; it is accepted only where a call handles caches
  * alone (pa_copy_blocks, pa_swap_blocks).  The FP8 decode and cache write take the
- * 16-bit type of q / out / key / value instead. */
-typedef enum { PA_FP16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+ * 16-bit type of q / out / key / value instead.  PA_FP32 names probabilities
+ * (pa_verify_drafts alone). */
+typedef enum { PA_FP16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_FP32 = 3 } pa_dtype;
 
 enum {
   PA_OK = 0,
@@ -71,6 +72,7 @@ enum {
 #define PA_DEVERR_TIMEOUT     0x10u /* a bounded wait gave up (about 1 s; prefill pipeline, decode
                                          split-KV merge): output invalid */
 #define PA_DEVERR_NO_BLOCKS   0x20u /* build_step: fewer free blocks than the step needs */
+#define PA_DEVERR_BAD_PROBS   0x40u /* verify_drafts: a row of probabilities without a positive one */
 
 /*
  * pa_reshape_and_cache -- write each new token's K and V rows into its cache slot.
@@ -390,6 +392,134 @@ int pa_prefill(const void* q, const void* k_cache, const void* v_cache,
                cudaStream_t stream);
 
 /*
+ * A decoding step that checks drafted tokens.  Each sequence feeds its last token and some
+ * drafted ones through the model at once; the calls below are the step's own work on paged
+ * caches: positions and the cache write (pa_rotary_append), attention of those few tokens over the
+ * long context (pa_decode_drafts), and the verdict on the drafts (pa_verify_drafts), whose
+ * context_next are the next step's lengths on the GPU.  pa_cross is the same attention without a
+ * mask, over an encoder's states.
+ *
+ * Common to them: sequence s owns rows query_start[s] .. query_start[s+1]-1 of the step's
+ * tensors (num_tokens rows in all), q_s of them.  query_start [num_seqs + 1] and context_lens
+ * [num_seqs] are int32 device arrays.  A sequence with an impossible span (query_start negative,
+ * decreasing or beyond num_tokens) is not read or written, and gets PA_DEVERR_BAD_CONTEXT.  Rows
+ * behind the last sequence (a padded batch) are left as they were.  A launch is a programmatic
+ * dependent of the kernel before it and reads everything only after that kernel has finished.
+ */
+/* Turns per token of `n` angles (radians per token, host), as pa_rotary and pa_rotary_append take
+ * them: freqs_out[i] = radians[i] / 2 pi in units of 2^-64, rounded, whole turns dropped (host;
+ * the caller copies them to the device).  |radians[i]| <= 10^6, else PA_ERR_ARG. */
+int pa_rotary_frequencies(const double* radians, int n, uint64_t* freqs_out);
+/*
+ * pa_rotary_append -- rotary positions of a step's new tokens, and their cache write.
+ *
+ * Row i of sequence s is at position p = context_lens[s] - q_s + i (context_lens count the
+ * step's tokens).  Pair j < rotary_dim / 2 of a head's first rotary_dim values is
+ * (x_j, x_{j + rotary_dim / 2}), or (x_2j, x_{2j+1}) if interleaved, and becomes
+ *   (a cos t - b sin t, b cos t + a sin t) * amplitude,   t = p * freqs[j] turns,
+ * in fp32, rounded to nearest-even; a head's other values are copied.  q's rows go to q_out; key's
+ * turned rows and value's rows go through the block table into the caches, at row p % B of block
+ * block_tables[s][p / B].  Positions are exact at any distance.
+ *
+ * q [num_tokens][Hq][d], key, value [num_tokens][Hkv][d], q_out as q: fp16 or bf16, heads
+ * contiguous, rows *_stride values apart (a multiple of 8, at least the row), so that they may be
+ * slices of one projection; bases 16-byte aligned.  q_out may be q itself, with q's stride.  rotary_dim: a
+ * multiple of 16 up to d.  freqs [rotary_dim / 2] device, 8-byte aligned.
+ * A sequence with q_s > context_lens[s] or a context beyond its table is skipped
+ * (PA_DEVERR_BAD_CONTEXT); where the block id is out of range K and V are skipped
+ * (PA_DEVERR_BAD_BLOCK), q is turned all the same.  No two rows may share a slot
+ * (copy-on-write first).
+ */
+int pa_rotary_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                     const void* value, int64_t value_stride, void* q_out, int64_t q_out_stride,
+                     void* k_cache, void* v_cache, const int32_t* block_tables,
+                     int max_blocks_per_seq, const int32_t* context_lens,
+                     const int32_t* query_start, const uint64_t* freqs, int rotary_dim,
+                     int interleaved, float amplitude, int num_seqs, int num_tokens,
+                     int num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
+                     int block_size, pa_dtype dtype, cudaStream_t stream);
+/* The same without the cache write, for caches of other formats: turned keys go to key_out, rows
+ * key_out_stride apart (which may be key itself, with its stride). */
+int pa_rotary(const void* q, int64_t q_stride, const void* key, int64_t key_stride, void* q_out,
+              int64_t q_out_stride, void* key_out, int64_t key_out_stride,
+              const int32_t* context_lens, const int32_t* query_start, const uint64_t* freqs,
+              int rotary_dim, int interleaved, float amplitude, int num_seqs, int num_tokens,
+              int num_q_heads, int num_kv_heads, int head_dim, pa_dtype dtype,
+              cudaStream_t stream);
+/*
+ * pa_decode_drafts -- causal attention of each sequence's newest tokens over its paged context,
+ * as pa_prefill, with the keys of a sequence split over the SMs: for a few tokens per sequence
+ * (drafts to be checked, the end of a prompt) over contexts of any length.
+ *
+ * q, out [num_tokens][Hq][d]; row i of sequence s is at position context_lens[s] - q_s + i, attends
+ * to positions up to its own, and its K/V rows are already in the cache (pa_rotary_append).
+ * scale > 0; Hq / Hkv <= 128; Hq <= 65536.  Accumulation fp32; fp16 weights keep what is above 2^-31
+ * of a row's largest.  V may hold magnitudes up to 2^100.  A key that a row does not attend to
+ * changes none of its bits, whatever it holds, NaN and infinities among it.
+ * The cuts depend on query_start, context_lens, max_blocks_per_seq, num_tokens and the head shape
+ * alone, never on where blocks sit.
+ * A sequence with rows and an invalid context (ctx < 1, ctx > T * B, q_s > ctx) gets zeros and
+ * PA_DEVERR_BAD_CONTEXT; a block id out of range gives zeros for the query tile that reads it
+ * and PA_DEVERR_BAD_BLOCK.
+ * workspace: device scratch of at least pa_split_workspace_size(...) bytes, 16-byte aligned, owned
+ * by the caller; its contents between calls do not matter.  Calls that may overlap must not share
+ * one.  PA_ERR_WORKSPACE if it is missing or too small.  num_seqs or num_tokens of 0: a no-op.
+ */
+int pa_decode_drafts(const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, const int32_t* query_start, int num_seqs,
+                     int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                     int block_size, int num_blocks, float scale, void* out, void* workspace,
+                     size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream);
+/*
+ * pa_cross -- attention of each sequence's rows to all context_lens[s] cached tokens: a decoder's
+ * tokens (one, or a whole prompt) over an encoder's states of another length, whose K/V rows lie
+ * in paged blocks (written once with pa_reshape_and_cache; shared by forks like any blocks).
+ * Arguments and rules of pa_decode_drafts, but: no mask; q_s and context_lens[s] are independent;
+ * a context of 0 gives zeros and no error (ctx < 0 or > T * B: zeros and PA_DEVERR_BAD_CONTEXT).
+ */
+int pa_cross(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+             int max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start,
+             int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+             int block_size, int num_blocks, float scale, void* out, void* workspace,
+             size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream);
+/* Bytes of workspace pa_decode_drafts and pa_cross need on the current device: it depends on
+ * its SM count and head_dim alone (152 SMs, head_dim 128: 41 MB). */
+size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
+/*
+ * pa_verify_drafts -- which drafted tokens stay, and the token after them.
+ *
+ * tokens [num_tokens] int32 are the step's inputs: a sequence's row 0 is its last token, rows 1 ..
+ * q_s - 1 its drafts.  target_probs [num_tokens][V] is the model's distribution after each row,
+ * draft_probs the same of the model that drafted: row i is what the draft in row i + 1 was drawn
+ * from (a sequence's last row is not read); NULL where each draft was certain (looked up, or the
+ * draft model's first choice).  Rows are *_stride values apart; fp32, fp16 or bf16 (`dtype`, both
+ * alike), in [0, 1] (what is negative or no number counts as 0, above 1 as 1); a row need not sum
+ * to 1.  uniforms [num_tokens] float32 in [0, 1).
+ *   Draft i + 1 is accepted while uniforms[i] * draft[i][x] < target[i][x], x = tokens[i + 1] (rows of
+ *   the sequence; draft 1 where NULL).  A token outside [0, V) is refused.
+ *   At the first refusal, row a: weights max(target[a] - draft[a], 0) (NULL: target[a] without x);
+ *   where all of them are zero, target[a].  With every draft accepted, a = q_s - 1: target[a].
+ *   The sampled token is the smallest t whose running sum of weights exceeds
+ *   uniforms[q_s - 1] times their sum.  Sums are exact in units of 2^-56: the token depends on no
+ *   order of addition.
+ * out_tokens [num_tokens]: rows 0 .. a - 1 the accepted drafts, row a the sampled token, -1 behind
+ * it.  emitted[s] = a + 1.  context_next[s] = context_lens[s] - q_s + emitted[s]: the tokens whose
+ * K/V rows stay (context_lens count the step's tokens; the next step adds its own); it may be
+ * context_lens itself.  A sequence without rows: 0 and context_lens[s].  A row a without a positive probability: -1 there,
+ * emitted[s] = a, PA_DEVERR_BAD_PROBS.  context_lens[s] < q_s: 0, context_lens[s],
+ * PA_DEVERR_BAD_CONTEXT.  V <= 2^20; out_tokens must not be tokens.  The launch lets none after it
+ * start early, so the lengths it writes may be read by any call that follows it in the stream.
+ * Blocks that a rejected draft had opened stay in the request's table (every call reads
+ * ceil(ctx / B) entries); pa_pool_truncate gives them back to the host pool.
+ */
+int pa_verify_drafts(const int32_t* tokens, const void* target_probs, int64_t target_stride,
+                     const void* draft_probs, int64_t draft_stride, const float* uniforms,
+                     const int32_t* query_start, const int32_t* context_lens, int num_seqs,
+                     int num_tokens, int vocab_size, int32_t* out_tokens, int32_t* emitted,
+                     int32_t* context_next, pa_dtype dtype, cudaStream_t stream);
+
+/*
  * pa_decode_append -- one whole decode step in one kernel: the cache write of every
  * sequence's newest token followed by pa_decode over contexts that include it.
  *
@@ -556,6 +686,12 @@ int pa_pool_append_slot(pa_pool* pool, int64_t seq_id, int64_t* slot_out, int32_
                         int32_t* cow_dst);
 /* The child shares every block of the parent (reference counts + 1). */
 int pa_pool_fork(pa_pool* pool, int64_t parent_id, int64_t child_id);
+/* Keep the sequence's first n_tokens tokens (0 <= n_tokens <= its length), those of rejected drafts
+ * say given up: its table keeps ceil(n / B) blocks, the others lose a reference and, at zero, go to
+ * the free-list tail in table order.  A last block that keeps fewer tokens than its digest names
+ * loses the digest (later tokens are written over the rest).  PA_ERR_ARG for n_tokens out of
+ * range, PA_ERR_WRONG_TIER for a sequence swapped out. */
+int pa_pool_truncate(pa_pool* pool, int64_t seq_id, int n_tokens);
 /* End a sequence; blocks whose count reaches zero go to the free-list tail in table order. */
 int pa_pool_free(pa_pool* pool, int64_t seq_id);
 /* Copy up to `cap` table entries into out; returns the table length or an error. */

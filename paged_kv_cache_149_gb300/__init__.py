@@ -38,10 +38,12 @@ DEVERR_BAD_SLOT = 0x4
 DEVERR_BAD_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_NO_BLOCKS = 0x20
+DEVERR_BAD_PROBS = 0x40
 
 PA_FP16 = 0
 PA_BF16 = 1
 PA_FP8_E4M3 = 2
+PA_FP32 = 3
 
 _c = ctypes
 _vp, _i32, _i64, _sz, _f32 = _c.c_void_p, _c.c_int, _c.c_int64, _c.c_size_t, _c.c_float
@@ -84,6 +86,19 @@ SIGNATURES = {
                                         _i32, _i32, _i32, _i32, _vp]),
     "pa_prefill": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                           _i32, _i32, _f32, _vp, _i32, _vp]),
+    "pa_rotary_frequencies": (_i32, [_vp, _i32, _vp]),
+    "pa_rotary": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _f32,
+                         _i32, _i32, _i32, _i32, _i32, _i32, _vp]),
+    "pa_rotary_append": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32,
+                                _vp, _vp, _vp, _i32, _i32, _f32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                _i32, _i32, _vp]),
+    "pa_decode_drafts": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                _i32, _i32, _f32, _vp, _vp, _sz, _i32, _vp]),
+    "pa_cross": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                        _i32, _f32, _vp, _vp, _sz, _i32, _vp]),
+    "pa_split_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "pa_verify_drafts": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp,
+                                _vp, _vp, _i32, _vp]),
     "pa_decode_workspace_size": (_sz, [_i32, _i32, _i32]),
     "pa_decode_timeline": (_i32, [_vp, _sz]),
     "pa_decode_fixed_scratch": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -101,6 +116,7 @@ SIGNATURES = {
     "pa_pool_append_slot": (_i32, [_vp, _i64, _c.POINTER(_i64), _c.POINTER(_c.c_int32),
                                    _c.POINTER(_c.c_int32)]),
     "pa_pool_fork": (_i32, [_vp, _i64, _i64]),
+    "pa_pool_truncate": (_i32, [_vp, _i64, _i32]),
     "pa_pool_free": (_i32, [_vp, _i64]),
     "pa_pool_block_table": (_i32, [_vp, _i64, _vp, _i32]),
     "pa_pool_context_len": (_i32, [_vp, _i64]),
@@ -990,6 +1006,294 @@ def swap_blocks_fp8_block(src, dst, block_mapping, stream=None, device=None):
     _check(st, "pa_swap_blocks_fp8_block")
 
 
+# ---- a decoding step that checks drafted tokens, and attention to an encoder's states ----
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, device="cuda"):
+    """(freqs, amplitude) for rotary and rotary_append: the turns per token of each pair, base **
+    (-2 i / rotary_dim) radians, as an int64 tensor [rotary_dim / 2] on `device` in units of 2^-64,
+    and the factor on cosines and sines.  `scaling` stretches them for contexts longer than the
+    model was trained on (a dict):
+      kind="linear", factor: f / factor;
+      kind="bands", factor, low, high, trained: f where the trained length holds more than `high`
+        turns, f / factor where fewer than `low`, blended by the number of turns between;
+      kind="ramp", factor, slow, fast, trained (and amplitude, 0.1 ln(factor) + 1 by default): f /
+        factor and f blended linearly in the pair's index between the indexes, rounded outwards,
+        whose pairs make `fast` and `slow` turns over the trained length."""
+    import math
+    import numpy as np
+    import torch
+    rd = int(rotary_dim)
+    _need(rd >= 2 and rd % 2 == 0, "rotary_dim must be even and positive")
+    base = float(base)
+    _need(math.isfinite(base) and base > 1.0, "base must be above 1")
+    f = np.array([base ** (-2.0 * i / rd) for i in range(rd // 2)], dtype=np.float64)
+    amplitude = 1.0
+    if scaling is not None:
+        how = dict(scaling)
+        kind, factor = how.pop("kind"), float(how.pop("factor"))
+        _need(math.isfinite(factor) and factor > 0.0, "factor must be positive")
+        if kind == "linear":
+            f = f / factor
+        elif kind == "bands":
+            low, high, trained = (float(how.pop(k)) for k in ("low", "high", "trained"))
+            _need(high > low, "high must be above low")
+            a = np.clip((trained * f / (2 * math.pi) - low) / (high - low), 0.0, 1.0)
+            f = (1 - a) * f / factor + a * f
+        elif kind == "ramp":
+            slow, fast, trained = (float(how.pop(k)) for k in ("slow", "fast", "trained"))
+            _need(slow > 0 and fast > 0 and trained > 0, "slow, fast and trained must be positive")
+
+            def index(turns):  # of the pair that makes so many turns over the trained length
+                return rd * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rd - 1)
+            a = np.clip((np.arange(rd // 2) - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+            f = a * f / factor + (1 - a) * f
+            amplitude = float(how.pop("amplitude", 0.1 * math.log(factor) + 1.0))
+        else:
+            raise ValueError(f"unknown scaling kind {kind!r}: linear, bands or ramp")
+        _need(not how, f"unknown scaling entries {sorted(how)}")
+    f = np.ascontiguousarray(f)
+    out = np.zeros(rd // 2, dtype=np.int64)
+    _check(lib().pa_rotary_frequencies(f.ctypes.data, rd // 2, out.ctypes.data), "pa_rotary_frequencies")
+    return torch.from_numpy(out).to(device), amplitude
+
+
+def _rows_ptr(t, name, heads, d, dtype, dev):
+    """(address, values from row to row) of a [rows, heads, d] tensor of `dtype` on CUDA device
+    number `dev` whose rows are contiguous, as slices of one projection's output are."""
+    if (t.dtype is not dtype or t.get_device() != dev or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d):
+        _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d, f"{name} must be [num_tokens, {heads}, {d}]")
+        _refuse(t.contiguous(), name, (dtype,), dev)
+    stride, sh, sd = t.stride()
+    if not (sd == 1 and (sh == d or heads == 1)):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if t.shape[0] <= 1:
+        stride = heads * d
+    return t.data_ptr(), stride
+
+
+def _freqs_ptr(freqs, dev):
+    T = _T or _torch()
+    half, = freqs.shape
+    return _ptr(freqs, "freqs", T.i64, dev), 2 * half
+
+
+@_on_its_device
+def rotary(q, key, context_lens, query_start, freqs, interleaved=False, amplitude=1.0, out=None,
+           key_out=None, stream=None, plan=False):
+    """Rotary positions of a step's new tokens: sequence s's rows query_start[s] ..
+    query_start[s+1]-1 of q [num_tokens, num_q_heads, d] and key [num_tokens, num_kv_heads, d] are
+    at positions context_lens[s] - q_len .. context_lens[s] - 1.  The first 2 * len(freqs) values
+    of each head are turned (rotary_frequencies), as halves or, interleaved, as neighbours.
+    Returns (out, key_out), which may be q and key themselves; rows behind the last sequence are left as
+    they were.  For caches that rotary_append does not write.  plan=True returns a Launch whose
+    runs return out (key_out must then be given)."""
+    T = _T or _torch()
+    dev, dt, i32 = _device_of(q, "q"), q.dtype, T.i32
+    ntok, hq, d = q.shape
+    hkv = key.shape[1]
+    n, = context_lens.shape
+    _need(key.shape[0] == ntok, "q and key must have as many rows")
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    _need(not (plan and key_out is None), "a planned rotary needs key_out")
+    if out is None:
+        out = _new_rows(q, stream)
+    if key_out is None:
+        key_out = _new_rows(key, stream)
+    _need(out.shape == q.shape and key_out.shape == key.shape, "out must match q, key_out key")
+    fptr, rd = _freqs_ptr(freqs, dev)
+    args = (*_rows_ptr(q, "q", hq, d, dt, dev), *_rows_ptr(key, "key", hkv, d, dt, dev),
+            *_rows_ptr(out, "out", hq, d, dt, dev), *_rows_ptr(key_out, "key_out", hkv, d, dt, dev),
+            _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
+            fptr, rd, int(bool(interleaved)), float(amplitude), n, ntok, hq, hkv, d, _code16(dt))
+    if plan:
+        return Launch("pa_rotary", args, out, keep=(q, key, key_out, context_lens, query_start, freqs))
+    st = lib().pa_rotary(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_rotary")
+    return out, key_out
+
+
+def _new_rows(t, stream):
+    """A new contiguous tensor of t's shape, allocated for the stream that the call runs on."""
+    T = _T or _torch()
+    if stream is None:
+        return T.module.empty(t.shape, dtype=t.dtype, device=t.device)
+    with T.module.cuda.stream(stream):
+        return T.module.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+@_on_its_device
+def rotary_append(q, key, value, k_cache, v_cache, block_tables, context_lens, query_start, freqs,
+                  interleaved=False, amplitude=1.0, out=None, stream=None, plan=False):
+    """rotary with the cache write, in one launch: the turned keys and the values go through the
+    block tables into the caches.  q, key and value may be slices of one projection's output
+    (heads contiguous, any distance from row to row that is a multiple of 8 values).  Returns the
+    turned q (out, which may be q itself).  plan=True returns a Launch instead of launching."""
+    T = _T or _torch()
+    dev, dt, i32 = _device_of(q, "q"), q.dtype, T.i32
+    ntok, hq, d = q.shape
+    n, width = block_tables.shape
+    nb, hkv, bs, d2 = shape = k_cache.shape
+    _need(d2 == d and v_cache.shape == shape, "shape mismatch")
+    _need(key.shape[0] == ntok and value.shape[0] == ntok, "q, key and value must have as many rows")
+    _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    if out is None:
+        out = _new_rows(q, stream)
+    _need(out.shape == q.shape, "out must match q")
+    fptr, rd = _freqs_ptr(freqs, dev)
+    args = (*_rows_ptr(q, "q", hq, d, dt, dev), *_rows_ptr(key, "key", hkv, d, dt, dev),
+            *_rows_ptr(value, "value", hkv, d, dt, dev), *_rows_ptr(out, "out", hq, d, dt, dev),
+            _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+            _ptr(block_tables, "block_tables", i32, dev), width,
+            _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
+            fptr, rd, int(bool(interleaved)), float(amplitude), n, ntok, nb, hq, hkv, d, bs, _code16(dt))
+    if plan:
+        return Launch("pa_rotary_append", args, out,
+                      keep=(q, key, value, k_cache, v_cache, block_tables, context_lens, query_start, freqs))
+    st = lib().pa_rotary_append(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_rotary_append")
+    return out
+
+
+def split_workspace_size(num_q_heads, num_kv_heads, head_dim):
+    """Bytes of workspace decode_drafts and cross need on the current device."""
+    n = lib().pa_split_workspace_size(num_q_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise PagedAttentionError(PA_ERR_ARG, "pa_split_workspace_size")
+    return n
+
+
+def make_split_workspace(num_q_heads, num_kv_heads, head_dim, device=None):
+    import torch
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        return torch.empty(split_workspace_size(num_q_heads, num_kv_heads, head_dim),
+                           dtype=torch.uint8, device=device)
+
+
+def _split_attention(name, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, out,
+                     workspace, stream, plan):
+    T = _T or _torch()
+    dev, i32, dt = _device_of(q, "q"), T.i32, q.dtype
+    ntok, hq, d = shape = q.shape
+    n, width = block_tables.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    _need(d2 == d and v_cache.shape == k_cache.shape, "shape mismatch")
+    _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    if out is None:
+        out = _empty_like(q, stream)
+    elif out.shape != shape or out.dtype is not dt:
+        raise ValueError("out must match q")
+    if workspace is None:
+        if stream is None:
+            workspace = make_split_workspace(hq, hkv, d, q.device)
+        else:
+            with T.module.cuda.stream(stream):  # (allocated for the stream that the call runs on)
+                workspace = make_split_workspace(hq, hkv, d, q.device)
+    args = (_ptr(q, "q", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+            _ptr(block_tables, "block_tables", i32, dev), width,
+            _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
+            n, ntok, hq, hkv, d, bs, nb, float(scale), _ptr(out, "out", dt, dev),
+            _ptr(workspace, "workspace", workspace.dtype, dev),
+            workspace.numel() * workspace.element_size(), _code16(dt))
+    if plan:
+        return Launch(name, args, out,
+                      keep=(q, k_cache, v_cache, block_tables, context_lens, query_start, workspace))
+    st = getattr(lib(), name)(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, name)
+    return out
+
+
+@_on_its_device
+def decode_drafts(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, out=None,
+                  workspace=None, stream=None, plan=False):
+    """Causal attention of each sequence's newest tokens (rows query_start[s] ..
+    query_start[s+1]-1 of q, at positions ctx - q_len .. ctx - 1, their K/V already in the cache)
+    over its paged context, the keys of a sequence split over the SMs: for a few tokens a sequence,
+    drafts to be checked say, where prefill would leave most SMs idle.  scale must be positive.
+    workspace: make_split_workspace.  plan=True returns a Launch instead of launching."""
+    return _split_attention("pa_decode_drafts", q, k_cache, v_cache, block_tables, context_lens,
+                            query_start, scale, out, workspace, stream, plan)
+
+
+@_on_its_device
+def cross(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, out=None,
+          workspace=None, stream=None, plan=False):
+    """Attention of each sequence's rows of q to all context_lens[s] cached tokens, without a mask:
+    a decoder's tokens over an encoder's states of another length (0 of them: zeros).  Otherwise
+    as decode_drafts."""
+    return _split_attention("pa_cross", q, k_cache, v_cache, block_tables, context_lens,
+                            query_start, scale, out, workspace, stream, plan)
+
+
+def _probs_ptr(t, name, dtype, dev):
+    """(address, values from row to row) of probabilities [rows, vocab]."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t.contiguous(), name, (dtype,), dev)
+    stride, sv = t.stride()
+    if sv != 1 and t.shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (stride if t.shape[0] > 1 else t.shape[1])
+
+
+@_on_its_device
+def verify_drafts(tokens, target_probs, draft_probs, uniforms, query_start, context_lens, out=None,
+                  emitted=None, context_next=None, stream=None, plan=False):
+    """Which drafted tokens stay, and the token after them.  tokens [num_tokens] int32: sequence
+    s's rows query_start[s] .. query_start[s+1]-1 are its last token and its drafts; target_probs
+    [num_tokens, vocab] the model's distribution after each row; draft_probs the same of the model
+    that drafted (row i is what row i + 1's token was drawn from), or None where each draft was
+    certain; uniforms [num_tokens] float32 in [0, 1).  A draft x in row i + 1 is accepted while
+    uniforms[i] * draft[i, x] < target[i, x]; then a token is drawn from max(target - draft, 0) of
+    the first row refused, or from the last row's target, by inversion with the sequence's last
+    uniform.  Returns (out [num_tokens]: accepted drafts, the drawn token, -1; emitted [num_seqs]:
+    tokens that came out; context_next [num_seqs]: context_lens - q_len + emitted, the tokens
+    whose K/V rows stay, which may be context_lens itself).  Rows of the probabilities may lie
+    farther apart than vocab.  plan=True returns a Launch whose runs return out (emitted and
+    context_next must then be given)."""
+    T = _T or _torch()
+    dev, i32 = _device_of(tokens, "tokens"), T.i32
+    ntok, = tokens.shape
+    n, = context_lens.shape
+    rows, vocab = target_probs.shape
+    dt = target_probs.dtype
+    _need(rows == ntok and uniforms.shape == (ntok,), "tokens, target_probs and uniforms must have as many rows")
+    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    _need(not plan or (emitted is not None and context_next is not None),
+          "a planned verify_drafts needs emitted and context_next")
+    code = PA_FP32 if dt is T.f32 else _code16(dt)
+    if out is None:
+        out = _empty_like(tokens, stream)
+    if emitted is None:
+        emitted = _empty_like(context_lens, stream)
+    if context_next is None:
+        context_next = _empty_like(context_lens, stream)
+    _need(out.shape == (ntok,) and emitted.shape == (n,) and context_next.shape == (n,),
+          "out must be [num_tokens], emitted and context_next [num_seqs]")
+    if draft_probs is None:
+        draft = (None, 0)
+    else:
+        _need(draft_probs.shape == (rows, vocab), "draft_probs must match target_probs")
+        draft = _probs_ptr(draft_probs, "draft_probs", dt, dev)
+    args = (_ptr(tokens, "tokens", i32, dev), *_probs_ptr(target_probs, "target_probs", dt, dev), *draft,
+            _ptr(uniforms, "uniforms", T.f32, dev), _ptr(query_start, "query_start", i32, dev),
+            _ptr(context_lens, "context_lens", i32, dev), n, ntok, vocab, _ptr(out, "out", i32, dev),
+            _ptr(emitted, "emitted", i32, dev), _ptr(context_next, "context_next", i32, dev), code)
+    if plan:
+        return Launch("pa_verify_drafts", args, out,
+                      keep=(tokens, target_probs, draft_probs, uniforms, query_start, context_lens, emitted,
+                            context_next))
+    st = lib().pa_verify_drafts(*args, _raw_stream(stream, dev))
+    if st < 0:
+        _check(st, "pa_verify_drafts")
+    return out, emitted, context_next
+
+
 @_on_first
 def copy_blocks(k_cache, v_cache, block_mapping, stream=None):
     """k_cache[dst] = k_cache[src] and v_cache[dst] = v_cache[src] for each (src, dst)."""
@@ -1129,6 +1433,10 @@ class BlockPool:
 
     def fork(self, parent, child):
         _check(lib().pa_pool_fork(self._h, int(parent), int(child)), "fork")
+
+    def truncate(self, seq, n_tokens):
+        """Keep the sequence's first n_tokens tokens (rejected drafts are given up)."""
+        _check(lib().pa_pool_truncate(self._h, int(seq), int(n_tokens)), "truncate")
 
     def free(self, seq):
         _check(lib().pa_pool_free(self._h, int(seq)), "free")

@@ -17,7 +17,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "pa_decode.cu", "pa_decode_fp8.cu", "pa_decode_int4.cu", "pa_decode_fp8_block.cu",
            "pa_decode_append.cu", "pa_decode_append_fp8.cu", "pa_decode_append_int4.cu", "pa_decode_timed.cu",
-           "pa_prefill.cu", "pa_prefill_fp8_block.cu", "pa_cache_ops.cu", "pa_fp8_block.cu", "pa_step.cu", "pa_fixed_scratch.cu", "pa_pool.cpp"]
+           "pa_prefill.cu", "pa_prefill_fp8_block.cu", "pa_cache_ops.cu", "pa_fp8_block.cu", "pa_step.cu", "pa_fixed_scratch.cu",
+           "pa_split_attention.cu", "pa_rotary.cu", "pa_verify.cu", "pa_pool.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -559,6 +559,236 @@ int pa_decode_append(const void* q, const void* key_new, const void* value_new, 
                      num_blocks, scale, out, workspace, workspace_bytes, dtype, stream);
 }
 
+namespace {
+
+// pa_decode_drafts and pa_cross: argument checks, then the launches.
+int split_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+               int max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start, int num_seqs,
+               int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+               float scale, void* out, void* workspace, size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream,
+               bool causal) {
+  if (num_seqs < 0 || num_tokens < 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      !shape_ok(num_kv_heads, head_dim, block_size) || num_q_heads < num_kv_heads ||
+      num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > 128 || num_q_heads > 65536 ||
+      !std::isfinite(scale) || !(scale > 0.f) || (dtype != PA_FP16 && dtype != PA_BF16))
+    return PA_ERR_ARG;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !out) return PA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < pa::split_workspace_bytes(di.sm_count, head_dim))
+    return PA_ERR_WORKSPACE;
+  pa::PrefillArgs a;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.out = out;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_query_len = 0;
+  a.scale = scale;
+  a.bf16 = dtype == PA_BF16;
+  a.err = di.err;
+  return pa::split_attention_launch(a, num_tokens, causal, workspace, di.sm_count, stream);
+}
+
+// What pa_rotary and pa_rotary_append share of their checks.
+bool rotary_shape_ok(int rotary_dim, float amplitude, int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                     int head_dim, pa_dtype dtype) {
+  return num_seqs >= 0 && num_tokens >= 0 && num_q_heads >= 1 && num_kv_heads >= 1 && num_q_heads <= 65536 &&
+         num_kv_heads <= 65536 && (head_dim == 64 || head_dim == 128) && rotary_dim >= 16 && rotary_dim <= head_dim &&
+         rotary_dim % 16 == 0 && std::isfinite(amplitude) && (dtype == PA_FP16 || dtype == PA_BF16);
+}
+// Rows of `heads` heads of 16-bit values, `stride` values apart, in 16-byte pieces.
+bool rows_ok(const void* base, int64_t stride, int heads, int head_dim) {
+  return base && aligned16(base) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * head_dim;
+}
+
+}  // namespace
+
+size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim) {
+  if (num_kv_heads < 1 || num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > 128 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  DeviceInfo di;
+  if (!device_info(&di)) return 0;
+  return pa::split_workspace_bytes(di.sm_count, head_dim);
+}
+
+int pa_decode_drafts(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                     int max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start, int num_seqs,
+                     int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                     float scale, void* out, void* workspace, size_t workspace_bytes, pa_dtype dtype,
+                     cudaStream_t stream) {
+  return split_call(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
+                    num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, out, workspace,
+                    workspace_bytes, dtype, stream, true);
+}
+
+int pa_cross(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+             int max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start, int num_seqs,
+             int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+             float scale, void* out, void* workspace, size_t workspace_bytes, pa_dtype dtype, cudaStream_t stream) {
+  return split_call(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
+                    num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, out, workspace,
+                    workspace_bytes, dtype, stream, false);
+}
+
+int pa_rotary_frequencies(const double* radians, int n, uint64_t* freqs_out) {
+  if (n < 0 || (n > 0 && (!radians || !freqs_out))) return PA_ERR_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!(std::fabs(radians[i]) <= 1e6)) return PA_ERR_ARG;
+  for (int i = 0; i < n; ++i) {
+    // radians / 2 pi in units of 2^-64: the 53-bit significand times the first 128 bits of 1 / 2 pi
+    // (which is kInv 2^-130), shifted into place with one rounding
+    const uint64_t kHi = 0xa2f9836e4e441529ull, kLo = 0xfc2757d1f534ddc0ull;
+    int e = 0;
+    const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(std::fabs(radians[i]), &e), 53));
+    const int shift = 130 - 64 - (e - 53);  // at least 99: |radians| < 2^20
+    const unsigned __int128 top = static_cast<unsigned __int128>(m) * kHi +
+                                  (static_cast<unsigned __int128>(m) * kLo >> 64);
+    uint64_t f = 0;
+    if (shift - 64 < 128) f = static_cast<uint64_t>(((top >> (shift - 65)) + 1) >> 1);
+    freqs_out[i] = radians[i] < 0 ? 0 - f : f;
+  }
+  return PA_OK;
+}
+
+int pa_rotary(const void* q, int64_t q_stride, const void* key, int64_t key_stride, void* q_out, int64_t q_out_stride,
+              void* key_out, int64_t key_out_stride, const int32_t* context_lens, const int32_t* query_start,
+              const uint64_t* freqs, int rotary_dim, int interleaved, float amplitude, int num_seqs, int num_tokens,
+              int num_q_heads, int num_kv_heads, int head_dim, pa_dtype dtype, cudaStream_t stream) {
+  if (!rotary_shape_ok(rotary_dim, amplitude, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, dtype))
+    return PA_ERR_ARG;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!context_lens || !query_start || !freqs || reinterpret_cast<uintptr_t>(freqs) % 8 != 0 ||
+      !rows_ok(q, q_stride, num_q_heads, head_dim) || !rows_ok(key, key_stride, num_kv_heads, head_dim) ||
+      !rows_ok(q_out, q_out_stride, num_q_heads, head_dim) || !rows_ok(key_out, key_out_stride, num_kv_heads, head_dim))
+    return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  pa::RotaryArgs a = {};
+  a.q = q;
+  a.key = key;
+  a.q_out = q_out;
+  a.key_out = key_out;
+  a.q_stride = q_stride;
+  a.key_stride = key_stride;
+  a.q_out_stride = q_out_stride;
+  a.key_out_stride = key_out_stride;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.freqs = freqs;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = 8;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.bf16 = dtype == PA_BF16;
+  a.amplitude = amplitude;
+  a.err = di.err;
+  return pa::rotary_launch(a, stream);
+}
+
+int pa_rotary_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride, const void* value,
+                     int64_t value_stride, void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                     const int32_t* query_start, const uint64_t* freqs, int rotary_dim, int interleaved,
+                     float amplitude, int num_seqs, int num_tokens, int num_blocks, int num_q_heads, int num_kv_heads,
+                     int head_dim, int block_size, pa_dtype dtype, cudaStream_t stream) {
+  if (!rotary_shape_ok(rotary_dim, amplitude, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, dtype) ||
+      !shape_ok(num_kv_heads, head_dim, block_size) || num_blocks < 1 || max_blocks_per_seq < 1)
+    return PA_ERR_ARG;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!context_lens || !query_start || !block_tables || !freqs || reinterpret_cast<uintptr_t>(freqs) % 8 != 0 ||
+      !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !rows_ok(q, q_stride, num_q_heads, head_dim) || !rows_ok(key, key_stride, num_kv_heads, head_dim) ||
+      !rows_ok(value, value_stride, num_kv_heads, head_dim) || !rows_ok(q_out, q_out_stride, num_q_heads, head_dim))
+    return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  pa::RotaryArgs a = {};
+  a.q = q;
+  a.key = key;
+  a.value = value;
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.q_stride = q_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.q_out_stride = q_out_stride;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.freqs = freqs;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.bf16 = dtype == PA_BF16;
+  a.amplitude = amplitude;
+  a.err = di.err;
+  return pa::rotary_launch(a, stream);
+}
+
+int pa_verify_drafts(const int32_t* tokens, const void* target_probs, int64_t target_stride, const void* draft_probs,
+                     int64_t draft_stride, const float* uniforms, const int32_t* query_start,
+                     const int32_t* context_lens, int num_seqs, int num_tokens, int vocab_size, int32_t* out_tokens,
+                     int32_t* emitted, int32_t* context_next, pa_dtype dtype, cudaStream_t stream) {
+  if (num_seqs < 0 || num_seqs > (1 << 24) || num_tokens < 0 || vocab_size < 1 || vocab_size > pa::verify_max_vocab() ||
+      (dtype != PA_FP16 && dtype != PA_BF16 && dtype != PA_FP32))
+    return PA_ERR_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!query_start || !context_lens || !emitted || !context_next) return PA_ERR_ARG;
+  const uintptr_t size = dtype == PA_FP32 ? 4 : 2;
+  if (num_tokens > 0 &&
+      (!tokens || !target_probs || !uniforms || !out_tokens || target_stride < vocab_size ||
+       reinterpret_cast<uintptr_t>(target_probs) % size != 0 || out_tokens == tokens ||
+       (draft_probs && (draft_stride < vocab_size || reinterpret_cast<uintptr_t>(draft_probs) % size != 0))))
+    return PA_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(&di)) return PA_ERR_CUDA;
+  pa::VerifyArgs a = {};
+  a.tokens = tokens;
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.uniforms = uniforms;
+  a.query_start = query_start;
+  a.context_lens = context_lens;
+  a.out_tokens = out_tokens;
+  a.emitted = emitted;
+  a.context_next = context_next;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.vocab = vocab_size;
+  a.value_bytes = static_cast<int>(size);
+  a.bf16 = dtype == PA_BF16;
+  a.err = di.err;
+  return pa::verify_drafts_launch(a, stream);
+}
+
 int pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_mapping, int num_pairs,
                    int num_blocks, int num_kv_heads, int head_dim, int block_size,
                    pa_dtype dtype, cudaStream_t stream) {

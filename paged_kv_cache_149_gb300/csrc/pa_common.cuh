@@ -21,6 +21,7 @@ constexpr unsigned kErrBadSlot = 0x4u;
 constexpr unsigned kErrBadPair = 0x8u;
 constexpr unsigned kErrTimeout = 0x10u;
 constexpr unsigned kErrNoBlocks = 0x20u;
+constexpr unsigned kErrBadProbs = 0x40u;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -61,6 +61,51 @@ int prefill_launch(const PrefillArgs& a, cudaStream_t stream);
 // The same over FP8 blocks with block scales [NB][Hkv]; q has num_tokens rows.
 int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* k_scales,
                              const float* v_scales, int sm_count, cudaStream_t stream);
+// Attention of PrefillArgs' rows with the keys split over the SMs (max_query_len unused): causal over
+// a sequence's own context, or over all of it.  workspace: split_workspace_bytes of the same grid.
+int split_attention_launch(const PrefillArgs& a, int num_tokens, bool causal, void* workspace, int sm_count,
+                           cudaStream_t stream);
+size_t split_workspace_bytes(int grid, int head_dim);
+
+struct RotaryArgs {
+  const void* q;
+  const void* key;
+  const void* value;  // null without the cache write
+  void* q_out;
+  void* key_out;  // null with it
+  void* k_cache;  // null without it
+  void* v_cache;
+  long long q_stride, key_stride, value_stride, q_out_stride, key_out_stride;  // values from row to row
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;
+  const uint64_t* freqs;
+  int num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, num_blocks;
+  int rotary_dim;
+  bool interleaved, bf16;
+  float amplitude;
+  unsigned* err;
+};
+int rotary_launch(const RotaryArgs& a, cudaStream_t stream);
+
+struct VerifyArgs {
+  const int32_t* tokens;
+  const void* target;
+  const void* draft;  // may be null
+  long long target_stride, draft_stride;  // values from row to row
+  const float* uniforms;
+  const int32_t* query_start;
+  const int32_t* context_lens;
+  int32_t* out_tokens;
+  int32_t* emitted;
+  int32_t* context_next;
+  int num_seqs, num_tokens, vocab, value_bytes;  // 4: float, 2: bf16 or fp16
+  bool bf16;
+  unsigned* err;
+};
+int verify_drafts_launch(const VerifyArgs& a, cudaStream_t stream);
+int verify_max_vocab();
+
 // q as [tokens][Hq][d] 16-bit for TMA loads of whole 128-row query tiles; false when the
 // group does not divide 128 or the driver's encoder is missing or rejects the tensor.
 bool q_tile_map(CUtensorMap* map, const void* q, int hq, int d, int g, long long tokens);

@@ -479,6 +479,25 @@ int pa_pool_fork(pa_pool* pool, int64_t parent_id, int64_t child_id) {
   return PA_OK;
 }
 
+int pa_pool_truncate(pa_pool* pool, int64_t seq_id, int n_tokens) {
+  if (!pool || n_tokens < 0) return PA_ERR_ARG;
+  auto it = pool->seqs.find(seq_id);
+  if (it == pool->seqs.end()) return PA_ERR_UNKNOWN_SEQ;
+  SeqState& st = it->second;
+  if (st.swapped) return PA_ERR_WRONG_TIER;
+  if (n_tokens > st.ctx) return PA_ERR_ARG;
+  if (n_tokens == st.ctx) return PA_OK;
+  const size_t keep = (static_cast<size_t>(n_tokens) + pool->block_size - 1) / pool->block_size;
+  for (size_t i = keep; i < st.table.size(); ++i)
+    if (--pool->gpu.refcount[st.table[i]] == 0) pool->gpu.push(st.table[i]);
+  st.table.resize(keep);
+  st.ctx = n_tokens;
+  // the rows behind n_tokens will be written over in place once the block has one owner
+  if (n_tokens % pool->block_size != 0 && pool->names.named(st.table.back()))
+    pool->names.unname(st.table.back());
+  return PA_OK;
+}
+
 int pa_pool_free(pa_pool* pool, int64_t seq_id) {
   if (!pool) return PA_ERR_ARG;
   auto it = pool->seqs.find(seq_id);
