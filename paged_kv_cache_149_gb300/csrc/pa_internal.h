@@ -62,10 +62,10 @@ int prefill_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_fp8_block_launch(const PrefillArgs& a, int num_tokens, const float* k_scales,
                              const float* v_scales, int sm_count, cudaStream_t stream);
 // Attention of PrefillArgs' rows with the keys split over the SMs (max_query_len unused): causal over
-// a sequence's own context, or over all of it.  workspace: split_workspace_bytes of the same grid.
+// a sequence's own context, or over all of it.  workspace: split_workspace_bytes of the same SMs.
 int split_attention_launch(const PrefillArgs& a, int num_tokens, bool causal, void* workspace, int sm_count,
                            cudaStream_t stream);
-size_t split_workspace_bytes(int grid, int head_dim);
+size_t split_workspace_bytes(int sm_count, int head_dim);
 
 struct RotaryArgs {
   const void* q;

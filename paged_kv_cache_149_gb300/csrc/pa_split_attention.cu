@@ -90,8 +90,8 @@ struct Params {
   const int32_t* query_start;  // [n + 1]
   uint8_t* out;
   Join* joins;    // [grid]
-  float4* sums;   // [grid][2][2 * kRows] (m, l, flags) of a cut item's rows
-  float4* parts;  // [grid][2][d / 4][2 * kRows] their O, row fastest
+  float4* sums;   // [grid][2][query tiles * kRows] (m, l, flags) of a cut item's rows
+  float4* parts;  // [grid][2][d / 4][query tiles * kRows] their O, row fastest
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group, tpt;  // tpt = tokens per query tile
   int max_blocks_per_seq, block_size, log2_block, num_blocks;
   uint32_t group_magic;  // ceil(2^16 / G): r / G = r * group_magic >> 16 for r < 128
@@ -151,28 +151,33 @@ __device__ __forceinline__ int first_masked(int ctx, int qlen, int tok0) {
   return (ctx - qlen + tok0 + 1) / kKeys;
 }
 
-template <int NT>
+template <int D, int NT>
 struct Shape {
   static constexpr int kThreads = NT == 2 ? 384 : 256;
-  static constexpr int kStages = NT == 2 ? 4 : 5;
+  static constexpr int kCtas = NT == 2 ? 1 : 2;  // per SM
+  static constexpr int kStages = NT == 2 ? 4 : (D == 128 ? 2 : 4);
 };
+// Two CTAs of 256 threads have 128 registers a thread; the softmax warpgroup takes kSoftmaxRegs, the
+// other keeps kOtherRegs (152 + 104 = 2 x 128).
+constexpr int kSoftmaxRegs = 152;
+constexpr int kOtherRegs = 104;
 
 template <int D, int NT>
 struct Smem {
-  static constexpr int kStages = Shape<NT>::kStages;
+  static constexpr int kStages = Shape<D, NT>::kStages;
   uint8_t q[NT][kRows * D * 2];        // K-major, 128-byte swizzle; 1024-byte aligned
   uint8_t k[kStages][kKeys * D * 2];   // [64-column half][64 keys][128 B]
   uint8_t v[kStages][kKeys * D * 2];
-  uint8_t stage[4 * NT][32 * 128];     // per softmax warp: 64 columns of its rows on their way out
+  uint8_t stage[4 * NT][32 * 64];      // per softmax warp: 32 columns of its rows on their way out
   Item item[kItems];
-  unsigned long long warp_sum[Shape<NT>::kThreads / 32];
+  unsigned long long warp_sum[Shape<D, NT>::kThreads / 32];
   int from[3], to[3];                  // the share: (sequence, item of it, key tile), and its end
   long long first_cut;                 // of the item that the share's end cuts: units before the cut
   unsigned long long item_full[kItems], item_free[kItems];
   unsigned long long q_full[NT], q_free[NT];
   unsigned long long k_full[kStages], v_full[kStages];
   unsigned long long s_full[NT][2], p_full[NT][2];
-  unsigned long long freed[kStages];   // P V of the stage's keys done, by every query tile
+  unsigned long long k_freed[kStages], v_freed[kStages];  // S, P V of them done, by every query tile
   // P V number i of the query tile done, at i % 2: the last two may both be under way when the
   // softmax waits, and a wait tells only neighbouring phases of a barrier apart
   unsigned long long pv_done[NT][2];
@@ -193,8 +198,9 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
 
 // Zeros for the values that are not finite in n 16-byte chunks of shared memory, 2048 bytes apart.
 template <typename T>
-__device__ __noinline__ void clear_odd(uint32_t at, int n) {
+__device__ __forceinline__ void clear_odd(uint32_t at, int n) {
   auto clean = [](uint32_t x) -> uint32_t { return x & ~((odd_halves<T>(x) >> 15) * 0xffffu); };
+#pragma unroll 1
   for (int c = 0; c < n; ++c, at += 2048) {
     const uint4 w = ld_shared16(at);
     st_shared16(at, make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w)));
@@ -209,27 +215,27 @@ __device__ __forceinline__ float fit(float x) {
   return x;
 }
 
-// What the values of V that went in as zeros add to a row at position pos: for each of the
-// columns c0 .. c0 + n - 1 the sum of those that are not finite among the keys it attends to.
-template <typename T>
-__device__ __noinline__ void add_odd(const Params& p, int s, int g, int first_key, int pos, int d, int c0,
-                                     int n, float* o) {
+// Adds what the values of V that went in as zeros give a row at position pos: to columns c0 .. c0 +
+// n - 1 of its row of out, those that are not finite among the keys it attends to.
+template <int D, typename T>
+__device__ __forceinline__ void add_odd(const Params& p, int s, int g, int first_key, int pos, int c0, int n, T* out) {
   const int32_t* trow = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+#pragma unroll 1
   for (int key = first_key; key <= pos; ++key) {
     const size_t block = static_cast<size_t>(trow[key >> p.log2_block]) * p.num_kv_heads + g;
-    const T* row = reinterpret_cast<const T*>(p.v_cache) +
-                   ((block << p.log2_block) + (key & (p.block_size - 1))) * d + c0;
-    for (int i = 0; i < n; ++i) {
+    const T* row = reinterpret_cast<const T*>(p.v_cache) + ((block << p.log2_block) + (key & (p.block_size - 1))) * D;
+#pragma unroll 1
+    for (int i = c0; i < c0 + n; ++i) {
       const float x = static_cast<float>(row[i]);
-      if (!(fabsf(x) < INFINITY)) o[i] += x;
+      if (!(fabsf(x) < INFINITY)) out[i] = from_float<T>(static_cast<float>(out[i]) + x);
     }
   }
 }
 
 template <int D, typename T, int NT, bool CAUSAL>
-__global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __grid_constant__ Params p) {
-  constexpr int kThreads = Shape<NT>::kThreads;
-  constexpr int kStages = Shape<NT>::kStages;
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) split_kernel(const __grid_constant__ Params p) {
+  constexpr int kThreads = Shape<D, NT>::kThreads;
+  constexpr int kStages = Shape<D, NT>::kStages;
   constexpr int kLoadWarp = 4 * NT;  // K, and the share's items; V and q by the next
   constexpr int kMmaWarp = kLoadWarp + 2;
   constexpr int CH = D / 8;              // 16-byte chunks of a 16-bit row
@@ -263,7 +269,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&sm.k_full[i]), 33);  // TMA expect-tx + 32 copy lanes
       mbar_init(smem_addr(&sm.v_full[i]), 33);
-      mbar_init(smem_addr(&sm.freed[i]), NT);
+      mbar_init(smem_addr(&sm.k_freed[i]), NT);
+      mbar_init(smem_addr(&sm.v_freed[i]), NT);
     }
     for (int t = 0; t < NT; ++t) {
       mbar_init(smem_addr(&sm.q_full[t]), 33);
@@ -397,6 +404,10 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
     if (lane == 0) mbar_arrive(smem_addr(&sm.item_free[j % kItems]));
   };
 
+  if (NT == 1) {
+    if (warp < 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  }
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     // ===== loaders: K and the share's items; V and q =====
     const bool is_v = warp == kLoadWarp + 1;
@@ -478,6 +489,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
             __syncwarp();
             if (!tma) {
               const int live = min(tpt, it.end - first) * G * CH;
+#pragma unroll 1
               for (int u = lane; u < live; u += 32) {
                 const int r = u / CH, c = u % CH;
                 const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
         for (int a = 0; a + 1 < kTableAhead; ++a) ahead[a] = ahead[a + 1];
         ahead[kTableAhead - 1] = lookup(kt + kTableAhead);
         const int st = num % kStages;
-        if (num >= kStages && !(ok = wwait(sm.freed[st], (num / kStages - 1) & 1))) break;
+        if (num >= kStages && !(ok = wwait(is_v ? sm.v_freed[st] : sm.k_freed[st], (num / kStages - 1) & 1))) break;
         const uint32_t kb = smem_addr(is_v ? sm.v[st] : sm.k[st]);
         unsigned long long& full = is_v ? sm.v_full[st] : sm.k_full[st];
         // lane b: rows of block b that lie inside the context; whole blocks come by TMA
@@ -532,10 +544,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
             tma_load_4d(kb + h * kHalf + b * B * 128, tmap, h * 64, 0, it.g, e, smem_addr(&full));
         }
         // the ragged block and blocks past the context: rows by cp.async, zero-filled
+#pragma unroll 1
         for (int b = 0; b < nbk; ++b) {
           if (whole >> b & 1) continue;
           const int rows = __shfl_sync(0xffffffffu, rows_b, b), e = __shfl_sync(0xffffffffu, my_e, b);
           const bool good = e >= 0 && e < p.num_blocks;
+#pragma unroll 1
           for (int u = lane; u < B * CH; u += 32) {
             const int r = u / CH, c = u % CH;
             const bool live = good && r < rows;
@@ -591,20 +605,20 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
       if (!(ok = wwait(sm.q_full[t], loads & 1))) break;
       ++loads;
       fence_async_smem();  // q rows that lanes copied -> tensor cores
-      auto key_ready = [&](uint32_t x) -> bool {
-        if (!wwait(sm.k_full[x % kStages], (x / kStages) & 1)) return false;
+      // K of key tile number x: S number sx of it, if this query tile needs it, and the stage back
+      auto keys = [&](uint32_t x, bool needed, uint32_t sx) -> bool {
+        const uint32_t st = x % kStages;
+        if (!wwait(sm.k_full[st], (x / kStages) & 1)) return false;
         fence_async_smem();  // rows the loader's lanes copied -> tensor cores
+        if (needed) issue_s(sx, st);
+        commit_el(smem_addr(&sm.k_freed[st]), el);
         return true;
       };
-      if (ntt > 0) {
-        if (!(ok = key_ready(num))) break;
-        issue_s(sn, num % kStages);
-      }
+      if (!(ok = keys(num, ntt > 0, sn))) break;
       if (ntt <= 1) commit_el(smem_addr(&sm.q_free[t]), el);
       for (int kt = 0; kt < n; ++kt, ++num) {
-        if (kt + 1 < ntt) {
-          if (!(ok = key_ready(num + 1))) break;
-          issue_s(sn + 1, (num + 1) % kStages);
+        if (kt + 1 < n) {
+          if (!(ok = keys(num + 1, kt + 1 < ntt, sn + 1))) break;
           if (kt + 2 == ntt) commit_el(smem_addr(&sm.q_free[t]), el);  // the item's last S
         }
         const uint32_t st = num % kStages;
@@ -616,10 +630,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
           issue_pv(sn, st, kt == 0);
           commit_el(smem_addr(&sm.pv_done[t][sn & 1]), el);
           ++sn;
-        } else if (!(ok = wwait(sm.k_full[st], (num / kStages) & 1))) {
-          break;
         }
-        commit_el(smem_addr(&sm.freed[st]), el);
+        commit_el(smem_addr(&sm.v_freed[st]), el);
       }
     }
     commit_el(smem_addr(&sm.fin[t]), el);  // every MMA this warp issued
@@ -747,18 +759,18 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
       const bool bad = flags & (kFlagBad << t);
       if (it.slot >= 0) {
         // ---- a piece: m, l and O for the join, row fastest: a warp's store is 512 bytes ----
-        const size_t row0 = static_cast<size_t>(it.slot) * (2 * kRows) + t * kRows + r;
+        const size_t row0 = static_cast<size_t>(it.slot) * (NT * kRows) + t * kRows + r;
         if (warp_ok) {
           p.sums[row0] = make_float4(m_run, l_run, __int_as_float((bad ? kFlagBad : 0) | (flags & kFlagOdd)), 0.f);
           if (ntt > 0) {
-            float4* to = p.parts + static_cast<size_t>(it.slot) * (D / 4) * (2 * kRows) + t * kRows + r;
+            float4* to = p.parts + static_cast<size_t>(it.slot) * (D / 4) * (NT * kRows) + t * kRows + r;
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
               float o[32];
               tmem_get32(tl + kColO + c0, o);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                to[(c0 / 4 + i) * (2 * kRows)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                to[(c0 / 4 + i) * (NT * kRows)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
         }
@@ -766,45 +778,42 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
       } else {
         item_done(j);
         if (warp_ok) {
-          // ---- out = O / l, through shared memory, 64 columns at a time, so that each store
-          // instruction of a warp writes whole 128-byte lines.  Row r's 16-byte chunk c sits at
-          // chunk c ^ (r % 8) of its 128-byte staging row: neither the writes nor the reads collide
-          // in a bank. ----
+          // ---- out = O / l, through shared memory, 32 columns at a time, so that each store
+          // instruction of a warp writes eight rows' 64 bytes.  Row r's 16-byte chunk c sits at
+          // chunk c ^ (r / 2 % 4) of its 64-byte staging row: neither the writes nor the reads
+          // collide in a bank. ----
           const bool good = it.ok && !bad;
           const bool odd = CAUSAL && good && (flags & kFlagOdd);
           const float inv = 1.f / l_run;
           const uint32_t stage = smem_addr(sm.stage[warp]);
-          const int ch = lane & 7;
+          const int ch = lane & 3;
           T* to = outp + (static_cast<size_t>(it.qs + it.tok0 + t * tpt) * p.num_q_heads + it.g * G) * D + ch * 8;
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 64) {
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            if (good) {  // (uniform over the warp)
+              tmem_get32(tl + kColO + c0, o);
 #pragma unroll
-            for (int c1 = 0; c1 < 64; c1 += 32) {
-              float o[32];
-              if (good) {  // (uniform over the warp)
-                tmem_get32(tl + kColO + c0 + c1, o);
+              for (int i = 0; i < 32; ++i) o[i] = fit<T>(o[i] * inv);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = fit<T>(o[i] * inv);
-              } else {
+              for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-              }
-#pragma unroll
-              for (int cc = 0; cc < 4; ++cc) {
-                uint4 w;
-                w.x = pack2<T>(o[8 * cc], o[8 * cc + 1]);
-                w.y = pack2<T>(o[8 * cc + 2], o[8 * cc + 3]);
-                w.z = pack2<T>(o[8 * cc + 4], o[8 * cc + 5]);
-                w.w = pack2<T>(o[8 * cc + 6], o[8 * cc + 7]);
-                st_shared16(stage + lane * 128 + (((c1 / 8 + cc) ^ (lane & 7)) << 4), w);
-              }
+            for (int cc = 0; cc < 4; ++cc) {
+              uint4 w;
+              w.x = pack2<T>(o[8 * cc], o[8 * cc + 1]);
+              w.y = pack2<T>(o[8 * cc + 2], o[8 * cc + 3]);
+              w.z = pack2<T>(o[8 * cc + 4], o[8 * cc + 5]);
+              w.w = pack2<T>(o[8 * cc + 6], o[8 * cc + 7]);
+              st_shared16(stage + lane * 64 + ((cc ^ ((lane >> 1) & 3)) << 4), w);
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = 4 * i + (lane >> 3), row = (r - lane) + rr;  // token tk of the tile, head row % G
+            for (int i = 0; i < 4; ++i) {
+              const int rr = 8 * i + (lane >> 2), row = (r - lane) + rr;  // token tk of the tile, head row % G
               const int tk = static_cast<int>((row * p.group_magic) >> 16);
-              const uint4 w = ld_shared16(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+              const uint4 w = ld_shared16(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
               if (tk < toks)
                 *reinterpret_cast<uint4*>(to + static_cast<size_t>(tk * (p.num_q_heads - G) + row) * D + c0) = w;
             }
@@ -814,13 +823,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
             // the values of V that went in as zeros (rare: a later draft's row is not finite)
             T* row = outp + ((static_cast<size_t>(it.qs + it.tok0 + t * tpt + tile_tok) * p.num_q_heads) + it.g * G +
                              r - tile_tok * G) * D;
-            for (int c0 = 0; c0 < D; c0 += 8) {
-              float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              add_odd<T>(p, it.s, it.g, masked * kKeys, pos, D, c0, 8, o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (!(o[i] == 0.f)) row[c0 + i] = from_float<T>(static_cast<float>(row[c0 + i]) + o[i]);
-            }
+            add_odd<D, T>(p, it.s, it.g, masked * kKeys, pos, 0, D, row);
           }
           __syncwarp();
         }
@@ -857,7 +860,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) split_kernel(const __g
 
 // The join of cut items: grid (CTAs of the launch before, query tiles, 16-column groups), a thread
 // per row.  Pieces are added in order of their keys.
-template <int D, typename T, bool CAUSAL>
+template <int D, typename T, int NT, bool CAUSAL>
 __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Params p) {
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -870,10 +873,10 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
   int flags = 0;
   // piece f: slot 1 of the first CTA, slot 0 of the others
   auto slot = [&](int f) -> size_t { return f == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + f); };
-  const int row = t * kRows + r;
+  const int at = t * kRows + r;
   float m = -INFINITY;
   for (int f = 0; f <= j.followers; ++f) {
-    const float4 x = p.sums[slot(f) * (2 * kRows) + row];
+    const float4 x = p.sums[slot(f) * (NT * kRows) + at];
     flags |= __float_as_int(x.z);
     if (x.y != 0.f) m = fmaxf(m, x.x);
   }
@@ -881,14 +884,14 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
   float4 o[4] = {};
 #pragma unroll 2
   for (int f = 0; f <= j.followers; ++f) {
-    const float4 x = p.sums[slot(f) * (2 * kRows) + row];
+    const float4 x = p.sums[slot(f) * (NT * kRows) + at];
     if (x.y == 0.f) continue;  // no key of the piece counts for this row: no O was written, or zeros
     const float w = ex2(x.x - m);
     l += x.y * w;
-    const float4* from = p.parts + slot(f) * (D / 4) * (2 * kRows) + row;
+    const float4* from = p.parts + slot(f) * (D / 4) * (NT * kRows) + at;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float4 v = from[(c4 + c) * (2 * kRows)];
+      const float4 v = from[(c4 + c) * (NT * kRows)];
       o[c].x += v.x * w;
       o[c].y += v.y * w;
       o[c].z += v.z * w;
@@ -907,29 +910,30 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
   if (flags & kFlagBad) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  } else if (CAUSAL && (flags & kFlagOdd)) {
-    add_odd<T>(p, j.s, j.g, first_masked(j.ctx, j.qlen, j.tok0) * kKeys,
-               j.ctx - j.qlen + j.tok0 + t * tpt + tok, D, 4 * c4, 16, x);
   }
   uint4 w[2];
   uint32_t* ww = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
   for (int i = 0; i < 8; ++i) ww[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
-  uint4* to = reinterpret_cast<uint4*>(
-      reinterpret_cast<T*>(p.out) +
-      (static_cast<size_t>(j.qs + j.tok0 + t * tpt + tok) * p.num_q_heads + j.g * G + r - tok * G) * D + 4 * c4);
+  T* row_out = reinterpret_cast<T*>(p.out) +
+               (static_cast<size_t>(j.qs + j.tok0 + t * tpt + tok) * p.num_q_heads + j.g * G + r - tok * G) * D;
+  uint4* to = reinterpret_cast<uint4*>(row_out + 4 * c4);
   to[0] = w[0];
   to[1] = w[1];
+  if (CAUSAL && (flags & kFlagOdd) && !(flags & kFlagBad))
+    add_odd<D, T>(p, j.s, j.g, first_masked(j.ctx, j.qlen, j.tok0) * kKeys, j.ctx - j.qlen + j.tok0 + t * tpt + tok,
+                  4 * c4, 16, row_out);
 }
 
 template <int D, typename T, int NT, bool CAUSAL>
-int launch(const Params& p, int grid, cudaStream_t stream) {
+int launch(const Params& p, int sm_count, cudaStream_t stream) {
+  const int grid = sm_count * Shape<D, NT>::kCtas;
   const size_t smem = sizeof(Smem<D, NT>) + 1024;
   auto* kern = split_kernel<D, T, NT, CAUSAL>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), smem)) return -3;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Shape<NT>::kThreads);
+  cfg.blockDim = dim3(Shape<D, NT>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -942,31 +946,31 @@ int launch(const Params& p, int grid, cudaStream_t stream) {
   cfg.gridDim = dim3(grid, NT, D / 16);
   cfg.blockDim = dim3(kRows);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<D, T, CAUSAL>, p) != cudaSuccess) return -3;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<D, T, NT, CAUSAL>, p) != cudaSuccess) return -3;
   return 0;
 }
 
 template <int D, typename T>
-int launch2(const Params& p, bool two, bool causal, int grid, cudaStream_t stream) {
+int launch2(const Params& p, bool two, bool causal, int sm_count, cudaStream_t stream) {
   if (causal)
-    return two ? launch<D, T, 2, true>(p, grid, stream) : launch<D, T, 1, true>(p, grid, stream);
-  return two ? launch<D, T, 2, false>(p, grid, stream) : launch<D, T, 1, false>(p, grid, stream);
+    return two ? launch<D, T, 2, true>(p, sm_count, stream) : launch<D, T, 1, true>(p, sm_count, stream);
+  return two ? launch<D, T, 2, false>(p, sm_count, stream) : launch<D, T, 1, false>(p, sm_count, stream);
 }
 
 size_t joins_bytes() { return sizeof(Join) * kMaxGrid; }
-size_t sums_bytes(int grid) { return sizeof(float4) * static_cast<size_t>(grid) * 2 * 2 * kRows; }
+// (two query tiles a CTA, or two CTAs an SM)
+size_t sums_bytes(int sm_count) { return sizeof(float4) * static_cast<size_t>(sm_count) * 2 * 2 * kRows; }
 
 }  // namespace split
 
-size_t split_workspace_bytes(int grid, int head_dim) {
-  return split::joins_bytes() + split::sums_bytes(grid) +
-         sizeof(float) * static_cast<size_t>(grid) * 2 * 2 * split::kRows * head_dim;
+size_t split_workspace_bytes(int sm_count, int head_dim) {
+  return split::joins_bytes() + split::sums_bytes(sm_count) +
+         sizeof(float) * static_cast<size_t>(sm_count) * 2 * 2 * split::kRows * head_dim;
 }
 
 int split_attention_launch(const PrefillArgs& a, int num_tokens, bool causal, void* workspace, int sm_count,
                            cudaStream_t stream) {
-  const int grid = sm_count;
-  if (grid > split::kMaxGrid) return -1;
+  if (2 * sm_count > split::kMaxGrid) return -1;
   split::Params p;
   if (!kv_cache_map(&p.kmap, a.k_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim) ||
       !kv_cache_map(&p.vmap, a.v_cache, 2, a.num_blocks, a.num_kv_heads, a.block_size, a.head_dim))
@@ -981,7 +985,7 @@ int split_attention_launch(const PrefillArgs& a, int num_tokens, bool causal, vo
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.joins = reinterpret_cast<split::Join*>(w);
   p.sums = reinterpret_cast<float4*>(w + split::joins_bytes());
-  p.parts = reinterpret_cast<float4*>(w + split::joins_bytes() + split::sums_bytes(grid));
+  p.parts = reinterpret_cast<float4*>(w + split::joins_bytes() + split::sums_bytes(sm_count));
   p.num_seqs = a.num_seqs;
   p.num_tokens = num_tokens;
   p.num_q_heads = a.num_q_heads;
@@ -1001,11 +1005,11 @@ int split_attention_launch(const PrefillArgs& a, int num_tokens, bool causal, vo
   // two query tiles per item, which share each key tile's loads, where sequences have the rows
   const bool two = static_cast<long long>(num_tokens) * p.group > static_cast<long long>(split::kRows) * a.num_seqs;
   if (a.head_dim == 128)
-    return a.bf16 ? split::launch2<128, __nv_bfloat16>(p, two, causal, grid, stream)
-                  : split::launch2<128, __half>(p, two, causal, grid, stream);
+    return a.bf16 ? split::launch2<128, __nv_bfloat16>(p, two, causal, sm_count, stream)
+                  : split::launch2<128, __half>(p, two, causal, sm_count, stream);
   if (a.head_dim == 64)
-    return a.bf16 ? split::launch2<64, __nv_bfloat16>(p, two, causal, grid, stream)
-                  : split::launch2<64, __half>(p, two, causal, grid, stream);
+    return a.bf16 ? split::launch2<64, __nv_bfloat16>(p, two, causal, sm_count, stream)
+                  : split::launch2<64, __half>(p, two, causal, sm_count, stream);
   return -1;
 }
 
