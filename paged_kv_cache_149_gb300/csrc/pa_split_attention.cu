@@ -57,7 +57,6 @@ using namespace tc;
 
 constexpr int kRows = 128;      // rows of a query tile (MMA M, tensor-memory lanes)
 constexpr int kKeys = 64;       // keys of a K/V tile (MMA N of S, K of P V)
-constexpr int kTableAhead = 4;  // tiles the loaders look block-table entries up ahead
 constexpr int kItems = 4;       // items in flight between the roles
 constexpr int kItemCost = 2;    // an item's start and end, in key tiles, for the shares
 constexpr int kLeastPiece = 4;  // key tiles: a cut that would leave fewer moves to the item's end
@@ -154,8 +153,8 @@ __device__ __forceinline__ int first_masked(int ctx, int qlen, int tok0) {
 template <int D, int NT>
 struct Shape {
   static constexpr int kThreads = NT == 2 ? 384 : 256;
-  static constexpr int kCtas = NT == 2 ? 1 : 2;  // per SM
-  static constexpr int kStages = NT == 2 ? 4 : (D == 128 ? 2 : 4);
+  static constexpr int kCtas = NT == 2 || D == 128 ? 1 : 2;  // per SM
+  static constexpr int kStages = NT == 2 ? 4 : (D == 128 ? 5 : 4);
 };
 // Two CTAs of 256 threads have 128 registers a thread; the softmax warpgroup takes kSoftmaxRegs, the
 // other keeps kOtherRegs (152 + 104 = 2 x 128).
@@ -238,6 +237,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
   constexpr int kStages = Shape<D, NT>::kStages;
   constexpr int kLoadWarp = 4 * NT;  // K, and the share's items; V and q by the next
   constexpr int kMmaWarp = kLoadWarp + 2;
+  constexpr int kQueryWarp = NT == 1 ? 7 : kLoadWarp + 1;  // loads q
   constexpr int CH = D / 8;              // 16-byte chunks of a 16-bit row
   constexpr int KS1 = D / 16;            // MMA k-steps of S = Q K^T
   constexpr int KS2 = kKeys / 16;        // MMA k-steps of P V
@@ -264,16 +264,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
   if (warp == kMmaWarp && lane == 0) {
     for (int i = 0; i < kItems; ++i) {
       mbar_init(smem_addr(&sm.item_full[i]), 1);
-      mbar_init(smem_addr(&sm.item_free[i]), 1 + NT + 4 * NT);  // V's loader, MMA, softmax warps
+      mbar_init(smem_addr(&sm.item_free[i]), kThreads / 32 - 1);  // every warp but K's loader
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&sm.k_full[i]), 33);  // TMA expect-tx + 32 copy lanes
-      mbar_init(smem_addr(&sm.v_full[i]), 33);
+      mbar_init(smem_addr(&sm.k_full[i]), 1);
+      mbar_init(smem_addr(&sm.v_full[i]), 1);
       mbar_init(smem_addr(&sm.k_freed[i]), NT);
       mbar_init(smem_addr(&sm.v_freed[i]), NT);
     }
     for (int t = 0; t < NT; ++t) {
-      mbar_init(smem_addr(&sm.q_full[t]), 33);
+      mbar_init(smem_addr(&sm.q_full[t]), 33);  // TMA expect-tx + 32 copy lanes
       mbar_init(smem_addr(&sm.q_free[t]), 1);
       mbar_init(smem_addr(&sm.fin[t]), 1);
       for (int b = 0; b < 2; ++b) {
@@ -404,14 +404,55 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
     if (lane == 0) mbar_arrive(smem_addr(&sm.item_free[j % kItems]));
   };
 
-  if (NT == 1) {
+  if (Shape<D, NT>::kCtas == 2) {
     if (warp < 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
+  // An item's q, load number `loads`: each query tile once the last item's S of it are done.  A whole one
+  // (tpt tokens x G heads = 128 rows, each token's G rows contiguous in q) by TMA, one copy per
+  // 64-column half; a tile that runs past its sequence by 16-byte copies of the rows it has (the others'
+  // S and O are garbage of their own lanes, which nothing reads).
+  auto load_q = [&](const Item& it, uint32_t loads) -> bool {
+    for (int t = 0; t < NT; ++t) {
+      if (loads > 0 && !wwait(sm.q_free[t], (loads - 1) & 1)) return false;
+      const int first = it.tok0 + t * tpt;
+      const bool tma = p.q_tma && first + tpt <= it.end;
+      if (lane == 0) {
+        sm.q_sent[t] = loads + 1;
+        mbar_arrive_expect_tx(smem_addr(&sm.q_full[t]), tma ? kRows * D * 2 : 0);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          if (tma)
+            tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, it.g * G, it.qs + first,
+                        smem_addr(&sm.q_full[t]));
+      }
+      __syncwarp();
+      if (!tma) {
+        const int live = min(tpt, it.end - first) * G * CH;
+#pragma unroll 4
+        for (int u = lane; u < live; u += 32) {
+          const int r = u / CH, c = u % CH;
+          const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
+          const uint8_t* src =
+              p.q + ((static_cast<size_t>(it.qs + first + tl) * p.num_q_heads + it.g * G + r - tl * G) * D + c * 8) * 2;
+          cp_async16(smem_addr(sm.q[t]) + swz(kRows, r, c), src, 16u);
+        }
+      }
+      cp_async_arrive(smem_addr(&sm.q_full[t]));
+    }
+    return true;
+  };
+  // The item's key tiles end here for its query tiles together.
+  auto item_end = [&](const Item& it, int* e0, int* e1) -> int {
+    *e0 = tiles_end<CAUSAL>(it, 0, tpt);
+    *e1 = NT == 2 ? tiles_end<CAUSAL>(it, 1, tpt) : *e0;
+    return max(*e0, *e1);
+  };
+
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    // ===== loaders: K and the share's items; V and q =====
+    // ===== loaders: K and the share's items; V =====
     const bool is_v = warp == kLoadWarp + 1;
-    const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
+    const uint32_t el = elect_one();
     const CUtensorMap* tmap = is_v ? &p.vmap : &p.kmap;
     const int B = p.block_size, nbk = kKeys >> p.log2_block;
     uint32_t num = 0, loads = 0;  // key tiles and q loads so far
@@ -452,7 +493,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
           it.end = min(sq.qlen, it.tok0 + per_item);
           it.t0 = tile;
           it.t1 = s == es && i == ei ? et : sq.tiles;
-          it.slot = tile > 0 ? 2 * static_cast<int>(blockIdx.x) : (it.t1 < sq.tiles ? 2 * static_cast<int>(blockIdx.x) + 1 : -1);
+          it.slot = tile > 0 ? 2 * static_cast<int>(blockIdx.x)
+                             : (it.t1 < sq.tiles ? 2 * static_cast<int>(blockIdx.x) + 1 : -1);
           ++i;
           tile = 0;
         }
@@ -464,102 +506,64 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
         __syncwarp();
       }
       if (!it.run) break;
-      const int e0 = tiles_end<CAUSAL>(it, 0, tpt), e1 = NT == 2 ? tiles_end<CAUSAL>(it, 1, tpt) : e0;
-      const int n = max(e0, e1);
+      int e0, e1;
+      const int n = item_end(it, &e0, &e1);
       if (is_v) {
         item_done(j);
-        if (n > it.t0) {
-          // q: each query tile once the last item's S of it are done.  A whole one (tpt tokens x G
-          // heads = 128 rows, each token's G rows contiguous in q) by TMA, one copy per 64-column
-          // half; a tile that runs past its sequence by 16-byte copies of the rows it has (the
-          // others' S and O are garbage of their own lanes, which nothing reads).
-          for (int t = 0; t < NT; ++t) {
-            if (loads > 0 && !(ok = wwait(sm.q_free[t], (loads - 1) & 1))) break;
-            const int first = it.tok0 + t * tpt;
-            const bool tma = p.q_tma && first + tpt <= it.end;
-            if (lane == 0) {
-              sm.q_sent[t] = loads + 1;
-              mbar_arrive_expect_tx(smem_addr(&sm.q_full[t]), tma ? kRows * D * 2 : 0);
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                if (tma)
-                  tma_load_3d(smem_addr(sm.q[t]) + h * kRows * 128, &p.qmap, h * 64, it.g * G,
-                              it.qs + first, smem_addr(&sm.q_full[t]));
-            }
-            __syncwarp();
-            if (!tma) {
-              const int live = min(tpt, it.end - first) * G * CH;
-#pragma unroll 1
-              for (int u = lane; u < live; u += 32) {
-                const int r = u / CH, c = u % CH;
-                const int tl = static_cast<int>((r * p.group_magic) >> 16);  // r / G
-                const uint8_t* src =
-                    p.q + ((static_cast<size_t>(it.qs + first + tl) * p.num_q_heads + it.g * G + r - tl * G) * D +
-                           c * 8) * 2;
-                cp_async16(smem_addr(sm.q[t]) + swz(kRows, r, c), src, 16u);
-              }
-            }
-            cp_async_arrive(smem_addr(&sm.q_full[t]));
-          }
-          if (!ok) break;
-          ++loads;
-        }
+        if (NT == 2 && n > it.t0 && !(ok = load_q(it, loads++))) break;
       }
       const int32_t* trow = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
-      auto lookup = [&](int kt) -> int {  // lane b: block b of the tile
-        const int lb = kt * nbk + lane;
-        return lane < nbk && kt < n && (static_cast<long long>(lb) << p.log2_block) < it.ctx ? trow[lb] : -1;
+      // Table entries, 32 blocks (4 to 16 key tiles) at once, a lane each, loaded as long before they are
+      // used: one lookup a tile, rotated through registers, held each tile up for the latency of the last.
+      const int per_batch = 32 >> (6 - p.log2_block);  // key tiles
+      auto lookup = [&](int first) -> int {
+        const long long lb = static_cast<long long>(first) * nbk + lane;
+        return first + lane / nbk < n && (lb << p.log2_block) < it.ctx ? trow[lb] : -1;
       };
-      int ahead[kTableAhead];
-#pragma unroll
-      for (int a = 0; a < kTableAhead; ++a) ahead[a] = lookup(it.t0 + a);
+      int entry = 0, coming = n > it.t0 ? lookup(it.t0) : -1;
+      uint32_t used = 0, there = 0;  // of the batch's blocks: hold keys; and have a block id
       for (int kt = it.t0; kt < n; ++kt, ++num) {
-        const int my_e = ahead[0];
-#pragma unroll
-        for (int a = 0; a + 1 < kTableAhead; ++a) ahead[a] = ahead[a + 1];
-        ahead[kTableAhead - 1] = lookup(kt + kTableAhead);
+        const int x = (kt - it.t0) & (per_batch - 1);
+        if (x == 0) {
+          entry = coming;
+          coming = lookup(kt + per_batch);
+          used = __ballot_sync(0xffffffffu, kt + lane / nbk < n &&
+                                                (static_cast<long long>(kt) * nbk + lane) << p.log2_block < it.ctx);
+          there = __ballot_sync(0xffffffffu, entry >= 0 && entry < p.num_blocks) & used;
+        }
         const int st = num % kStages;
         if (num >= kStages && !(ok = wwait(is_v ? sm.v_freed[st] : sm.k_freed[st], (num / kStages - 1) & 1))) break;
-        const uint32_t kb = smem_addr(is_v ? sm.v[st] : sm.k[st]);
-        unsigned long long& full = is_v ? sm.v_full[st] : sm.k_full[st];
-        // lane b: rows of block b that lie inside the context; whole blocks come by TMA
-        const int rows_b = lane < nbk ? min(B, max(0, it.ctx - (kt * nbk + lane) * B)) : 0;
-        const bool there = my_e >= 0 && my_e < p.num_blocks;
-        const uint32_t whole = __ballot_sync(0xffffffffu, rows_b == B && there);
-        if (__any_sync(0xffffffffu, rows_b > 0 && !there) && lane == 0) {
+        const uint32_t to = smem_addr(is_v ? sm.v[st] : sm.k[st]);
+        const uint32_t full = smem_addr(is_v ? &sm.v_full[st] : &sm.k_full[st]);
+        // the blocks that hold keys of the context, whole: what lies behind the context is masked (K), or
+        // cleared before it is used (V)
+        const uint32_t mask = there >> (x * nbk) & ((1u << nbk) - 1);
+        if ((used & ~there) >> (x * nbk) & ((1u << nbk) - 1) && lane == 0) {
           // (for the query tiles that need these keys: before the keys are announced to them)
           atomicOr(&sm.item[j % kItems].flags, (kt < e0 ? kFlagBad : 0) | (NT == 2 && kt < e1 ? kFlagBad << 1 : 0));
           atomicOr(p.err, kErrBadBlock);
         }
         if (lane == 0) {
           sm.sent[is_v] = num + 1;
-          mbar_arrive_expect_tx(smem_addr(&full), static_cast<uint32_t>(__popc(whole)) * B * D * 2);
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * B * D * 2);
         }
         __syncwarp();
-        {
-          constexpr int NH = D / 64;  // lane (b, h) copies block b's 64-column half h
-          const int b = lane / NH, h = lane % NH;
-          const int e = __shfl_sync(0xffffffffu, my_e, b < nbk ? b : 0);
-          if (b < nbk && (whole >> b & 1))
-            tma_load_4d(kb + h * kHalf + b * B * 128, tmap, h * 64, 0, it.g, e, smem_addr(&full));
+        for (uint32_t left = mask; left; left &= left - 1) {
+          const int b = __ffs(left) - 1, e = __shfl_sync(0xffffffffu, entry, x * nbk + b);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)  // 64-column halves
+            tma_load_4d_el(to + h * kHalf + b * B * 128, tmap, h * 64, 0, it.g, e, full, el);
         }
-        // the ragged block and blocks past the context: rows by cp.async, zero-filled
-#pragma unroll 1
-        for (int b = 0; b < nbk; ++b) {
-          if (whole >> b & 1) continue;
-          const int rows = __shfl_sync(0xffffffffu, rows_b, b), e = __shfl_sync(0xffffffffu, my_e, b);
-          const bool good = e >= 0 && e < p.num_blocks;
-#pragma unroll 1
-          for (int u = lane; u < B * CH; u += 32) {
-            const int r = u / CH, c = u % CH;
-            const bool live = good && r < rows;
-            const size_t src =
-                (((static_cast<size_t>(live ? e : 0) * p.num_kv_heads + it.g) * B + (live ? r : 0)) * D + c * 8) * 2;
-            cp_async16(kb + swz(kKeys, b * B + r, c), cache + src, live ? 16u : 0u);
-          }
-        }
-        cp_async_arrive(smem_addr(&full));
       }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (NT == 1 && warp == kQueryWarp) {
+    Item it;
+    uint32_t loads = 0;
+    for (int j = 0; item_get(j, it) && it.run; ++j) {
+      item_done(j);
+      int e0, e1;
+      if (item_end(it, &e0, &e1) > it.t0 && !load_q(it, loads++)) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kMmaWarp && warp < kMmaWarp + NT) {
@@ -658,15 +662,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
         const int b = sn & 1, kt = it.t0 + k;
         if (!(ok = wwait(sm.s_full[t][b], (sn >> 1) & 1))) break;
         tc_fence_after();
-        if (CAUSAL && kt >= masked) {
-          // V of this tile without what is not finite (by each warpgroup, whose P V follows: the
-          // second finds zeros, or writes the same ones)
+        const int rest = it.ctx - kt * kKeys;  // keys of this tile that the context holds, or more
+        if (rest < kKeys || (CAUSAL && kt >= masked)) {
+          // V of this tile without rows behind the context and without what is not finite where a row
+          // does not attend to it (by each warpgroup, whose P V follows: the second finds zeros, or
+          // writes the same ones)
           const uint32_t x = num + k, st = x % kStages;
           if (!(ok = wwait(sm.v_full[st], (x / kStages) & 1))) break;
+          if (rest < kKeys) {
+            const uint32_t from = smem_addr(sm.v[st]) + (r & 7) * 16;
+            for (int key = rest + (r >> 3); key < kKeys; key += 16)
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h) st_shared16(from + h * kHalf + key * 128, make_uint4(0, 0, 0, 0));
+          }
+        }
+        if (CAUSAL && kt >= masked) {
+          const uint32_t st = (num + k) % kStages;
           const uint32_t at = smem_addr(sm.v[st]) + r * 16;
           uint32_t odd = 0;
 #pragma unroll
           for (int c = 0; c < static_cast<int>(kStageBytes / 2048); ++c) {
+            if ((r >> 3) + (c & 3) * 16 >= rest) continue;  // (behind the context: zeros)
             const uint4 w = ld_shared16(at + c * 2048);
             odd |= odd_halves<T>(w.x) | odd_halves<T>(w.y) | odd_halves<T>(w.z) | odd_halves<T>(w.w);
           }
@@ -676,8 +692,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
             __threadfence_block();
             clear_odd<T>(at, kStageBytes / 2048);
           }
-          fence_async_smem();
         }
+        if (rest < kKeys || (CAUSAL && kt >= masked)) fence_async_smem();
         if (warp_ok) {
           float sv[kKeys];
           tmem_get64(tl + b * kColS, sv);

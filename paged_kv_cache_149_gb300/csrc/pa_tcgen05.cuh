@@ -242,5 +242,18 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   return v;
 }
 
+// tma_load_4d issued by the lane whose `el` is set, the whole warp running the code around it (as
+// mma_el): a copy issued under a branch of one lane, or by lanes with coordinates of their own, takes that
+// warp about 100 cycles.
+__device__ __forceinline__ void tma_load_4d_el(uint32_t dst, const void* map, int x, int y, int z, int w,
+                                               uint32_t bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(el)
+      : "memory");
+}
+
 }  // namespace tc
 }  // namespace pa
