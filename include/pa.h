@@ -501,7 +501,7 @@ size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
  *   At the first refusal, row a: weights max(target[a] - draft[a], 0) (NULL: target[a] without x);
  *   where all of them are zero, target[a].  With every draft accepted, a = q_s - 1: target[a].
  *   The sampled token is the smallest t whose running sum of weights exceeds
- *   uniforms[q_s - 1] times their sum.  Sums are exact in units of 2^-56: the token depends on no
+ *   uniforms[q_s - 1] times their sum.  Sums are exact in units of 2^-54: the token depends on no
  *   order of addition.
  * out_tokens [num_tokens]: rows 0 .. a - 1 the accepted drafts, row a the sampled token, -1 behind
  * it.  emitted[s] = a + 1.  context_next[s] = context_lens[s] - q_s + emitted[s]: the tokens whose

@@ -784,6 +784,7 @@ int pa_verify_drafts(const int32_t* tokens, const void* target_probs, int64_t ta
   a.num_tokens = num_tokens;
   a.vocab = vocab_size;
   a.value_bytes = static_cast<int>(size);
+  a.sm_count = di.sm_count;
   a.bf16 = dtype == PA_BF16;
   a.err = di.err;
   return pa::verify_drafts_launch(a, stream);

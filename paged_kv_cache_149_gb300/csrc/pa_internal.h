@@ -100,6 +100,7 @@ struct VerifyArgs {
   int32_t* emitted;
   int32_t* context_next;
   int num_seqs, num_tokens, vocab, value_bytes;  // 4: float, 2: bf16 or fp16
+  int sm_count;
   bool bf16;
   unsigned* err;
 };
