@@ -1132,23 +1132,36 @@ def rotary_append(q, key, value, k_cache, v_cache, block_tables, context_lens, q
     turned q (out, which may be q itself).  plan=True returns a Launch instead of launching."""
     T = _T or _torch()
     dev, dt, i32 = _device_of(q, "q"), q.dtype, T.i32
-    ntok, hq, d = q.shape
+    ntok, hq, d = shape = q.shape
     n, width = block_tables.shape
-    nb, hkv, bs, d2 = shape = k_cache.shape
-    _need(d2 == d and v_cache.shape == shape, "shape mismatch")
-    _need(key.shape[0] == ntok and value.shape[0] == ntok, "q, key and value must have as many rows")
-    _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
-    _need(query_start.shape == (n + 1,), "query_start must be [num_seqs + 1]")
+    nb, hkv, bs, d2 = cache = k_cache.shape
+    kv = (ntok, hkv, d)
     if out is None:
         out = _new_rows(q, stream)
-    _need(out.shape == q.shape, "out must match q")
-    fptr, rd = _freqs_ptr(freqs, dev)
-    args = (*_rows_ptr(q, "q", hq, d, dt, dev), *_rows_ptr(key, "key", hkv, d, dt, dev),
-            *_rows_ptr(value, "value", hkv, d, dt, dev), *_rows_ptr(out, "out", hq, d, dt, dev),
-            _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+    half, = freqs.shape
+    if not (key.shape == kv and value.shape == kv and out.shape == shape and d2 == d and v_cache.shape == cache
+            and context_lens.shape == (n,) and query_start.shape == (n + 1,)):
+        _need(key.shape == kv and value.shape == kv, "key and value must be [num_tokens, num_kv_heads, head_dim]")
+        _need(out.shape == shape, "out must match q")
+        _need(d2 == d and v_cache.shape == cache, "shape mismatch")
+        _need(context_lens.shape == (n,), "block_tables must be [num_seqs, T], context_lens [num_seqs]")
+        _need(False, "query_start must be [num_seqs + 1]")
+    q0, q1, q2 = q.stride()
+    k0, k1, k2 = key.stride()
+    v0, v1, v2 = value.stride()
+    o0, o1, o2 = out.stride()
+    if (q2 == k2 == v2 == o2 == 1 and q1 == k1 == v1 == o1 == d and ntok > 1 and key.dtype is dt
+            and value.dtype is dt and out.dtype is dt and key.get_device() == dev and value.get_device() == dev
+            and out.get_device() == dev):
+        rows = (q.data_ptr(), q0, key.data_ptr(), k0, value.data_ptr(), v0, out.data_ptr(), o0)
+    else:  # (one row, one head, or something to refuse)
+        rows = (*_rows_ptr(q, "q", hq, d, dt, dev), *_rows_ptr(key, "key", hkv, d, dt, dev),
+                *_rows_ptr(value, "value", hkv, d, dt, dev), *_rows_ptr(out, "out", hq, d, dt, dev))
+    args = (*rows, _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
             _ptr(block_tables, "block_tables", i32, dev), width,
             _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
-            fptr, rd, int(bool(interleaved)), float(amplitude), n, ntok, nb, hq, hkv, d, bs, _code16(dt))
+            _ptr(freqs, "freqs", T.i64, dev), 2 * half, 1 if interleaved else 0, amplitude, n, ntok, nb, hq, hkv, d, bs,
+            _code16(dt))
     if plan:
         return Launch("pa_rotary_append", args, out,
                       keep=(q, key, value, k_cache, v_cache, block_tables, context_lens, query_start, freqs))
@@ -1194,12 +1207,24 @@ def _split_attention(name, q, k_cache, v_cache, block_tables, context_lens, quer
         else:
             with T.module.cuda.stream(stream):  # (allocated for the stream that the call runs on)
                 workspace = make_split_workspace(hq, hkv, d, q.device)
-    args = (_ptr(q, "q", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
-            _ptr(block_tables, "block_tables", i32, dev), width,
-            _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
-            n, ntok, hq, hkv, d, bs, nb, float(scale), _ptr(out, "out", dt, dev),
-            _ptr(workspace, "workspace", workspace.dtype, dev),
-            workspace.numel() * workspace.element_size(), _code16(dt))
+    if (k_cache.dtype is dt and v_cache.dtype is dt and block_tables.dtype is i32 and context_lens.dtype is i32
+            and query_start.dtype is i32 and out.dtype is dt
+            and k_cache.get_device() == dev and v_cache.get_device() == dev and block_tables.get_device() == dev
+            and context_lens.get_device() == dev and query_start.get_device() == dev and out.get_device() == dev
+            and workspace.get_device() == dev
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and query_start.is_contiguous()
+            and out.is_contiguous() and workspace.is_contiguous()):
+        args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), width,
+                context_lens.data_ptr(), query_start.data_ptr(), n, ntok, hq, hkv, d, bs, nb, scale, out.data_ptr(),
+                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _code16(dt))
+    else:  # (says which one and why)
+        for t, what, kind in ((q, "q", dt), (k_cache, "k_cache", dt), (v_cache, "v_cache", dt),
+                              (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+                              (query_start, "query_start", i32), (out, "out", dt),
+                              (workspace, "workspace", workspace.dtype)):
+            _ptr(t, what, kind, dev)
+        raise ValueError("unsupported arguments")
     if plan:
         return Launch(name, args, out,
                       keep=(q, k_cache, v_cache, block_tables, context_lens, query_start, workspace))
@@ -1280,10 +1305,21 @@ def verify_drafts(tokens, target_probs, draft_probs, uniforms, query_start, cont
     else:
         _need(draft_probs.shape == (rows, vocab), "draft_probs must match target_probs")
         draft = _probs_ptr(draft_probs, "draft_probs", dt, dev)
-    args = (_ptr(tokens, "tokens", i32, dev), *_probs_ptr(target_probs, "target_probs", dt, dev), *draft,
-            _ptr(uniforms, "uniforms", T.f32, dev), _ptr(query_start, "query_start", i32, dev),
-            _ptr(context_lens, "context_lens", i32, dev), n, ntok, vocab, _ptr(out, "out", i32, dev),
-            _ptr(emitted, "emitted", i32, dev), _ptr(context_next, "context_next", i32, dev), code)
+    f32 = T.f32
+    if not (tokens.dtype is i32 and uniforms.dtype is f32 and query_start.dtype is i32 and context_lens.dtype is i32
+            and out.dtype is i32 and emitted.dtype is i32 and context_next.dtype is i32
+            and uniforms.get_device() == dev and query_start.get_device() == dev and context_lens.get_device() == dev
+            and out.get_device() == dev and emitted.get_device() == dev and context_next.get_device() == dev
+            and tokens.is_contiguous() and uniforms.is_contiguous() and query_start.is_contiguous()
+            and context_lens.is_contiguous() and out.is_contiguous() and emitted.is_contiguous()
+            and context_next.is_contiguous()):  # (says which one and why)
+        for t, what, kind in ((tokens, "tokens", i32), (uniforms, "uniforms", f32), (query_start, "query_start", i32),
+                              (context_lens, "context_lens", i32), (out, "out", i32), (emitted, "emitted", i32),
+                              (context_next, "context_next", i32)):
+            _ptr(t, what, kind, dev)
+    args = (tokens.data_ptr(), *_probs_ptr(target_probs, "target_probs", dt, dev), *draft, uniforms.data_ptr(),
+            query_start.data_ptr(), context_lens.data_ptr(), n, ntok, vocab, out.data_ptr(), emitted.data_ptr(),
+            context_next.data_ptr(), code)
     if plan:
         return Launch("pa_verify_drafts", args, out,
                       keep=(tokens, target_probs, draft_probs, uniforms, query_start, context_lens, emitted,
