@@ -195,17 +195,6 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
   return ((w & kExp) + kOne) & 0x80008000u;  // (an exponent of all ones carries into the sign's place)
 }
 
-// Zeros for the values that are not finite in n 16-byte chunks of shared memory, 2048 bytes apart.
-template <typename T>
-__device__ __forceinline__ void clear_odd(uint32_t at, int n) {
-  auto clean = [](uint32_t x) -> uint32_t { return x & ~((odd_halves<T>(x) >> 15) * 0xffffu); };
-#pragma unroll 1
-  for (int c = 0; c < n; ++c, at += 2048) {
-    const uint4 w = ld_shared16(at);
-    st_shared16(at, make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w)));
-  }
-}
-
 // A finished value as T holds it.  Rounded weights over the sum of unrounded ones may lift an average
 // of f16's largest values past them: such become the largest, infinities stay.
 template <typename T>
@@ -442,6 +431,48 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
     }
     return true;
   };
+  // V of a key tile before P V: rows behind the context become zeros, and so do values that are not finite
+  // from the first tile on that not every row attends to all of (a weight of zero would spread them).
+  // By every warp whose P V follows, so that one finds the zeros of another, or writes the same.  (In
+  // the softmax, which has more threads; of two query tiles in the MMA warps, since there the softmax's
+  // registers would spill: 460 -> 510 us on 6 x 900..2048 rows over 2000..8192 keys.)
+  constexpr bool kTidySoftmax = NT == 1;
+  auto untidy = [&](const Item& it, int kt) -> bool {
+    return it.ctx - kt * kKeys < kKeys || (CAUSAL && kt >= first_masked(it.ctx, it.qlen, it.tok0));
+  };
+  auto tidy = [&](const Item& it, int j, int kt, uint32_t st, int me, auto all) {
+    constexpr int kAll = decltype(all)::value;  // threads that share the work
+    const int rest = it.ctx - kt * kKeys;       // keys of this tile that the context holds, or more
+    const uint32_t v = smem_addr(sm.v[st]);
+#pragma unroll 1
+    for (int key = max(rest, 0) + (me >> 3); key < kKeys; key += kAll / 8)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        st_shared16(v + (me & 7) * 16 + h * kHalf + key * 128, make_uint4(0, 0, 0, 0));
+    if (CAUSAL && kt >= first_masked(it.ctx, it.qlen, it.tok0)) {
+      const uint32_t at = v + me * 16;
+      uint32_t odd = 0;
+#pragma unroll 4
+      for (int c = 0; c < static_cast<int>(kStageBytes / 16 / kAll); ++c) {
+        if ((me + c * kAll) % (kHalf / 16) / 8 >= rest) continue;  // (behind the context: zeros)
+        const uint4 w = ld_shared16(at + c * kAll * 16);
+        odd |= odd_halves<T>(w.x) | odd_halves<T>(w.y) | odd_halves<T>(w.z) | odd_halves<T>(w.w);
+      }
+      if (odd) {
+        // (the flag first: who finds the zeros has to find it)
+        atomicOr(&sm.item[j % kItems].flags, kFlagOdd);
+        __threadfence_block();
+        auto clean = [](uint32_t x) -> uint32_t { return x & ~((odd_halves<T>(x) >> 15) * 0xffffu); };
+#pragma unroll 1
+        for (int c = 0; c < static_cast<int>(kStageBytes / 16 / kAll); ++c) {
+          const uint4 w = ld_shared16(at + c * kAll * 16);
+          st_shared16(at + c * kAll * 16, make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w)));
+        }
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+  };
   // The item's key tiles end here for its query tiles together.
   auto item_end = [&](const Item& it, int* e0, int* e1) -> int {
     *e0 = tiles_end<CAUSAL>(it, 0, tpt);
@@ -629,6 +660,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
         if (!(ok = wwait(sm.v_full[st], (num / kStages) & 1))) break;
         if (kt < ntt) {
           if (!(ok = wwait(sm.p_full[t][sn & 1], (sn >> 1) & 1))) break;
+          if (!kTidySoftmax && untidy(it, it.t0 + kt))
+            tidy(it, j, it.t0 + kt, st, lane, std::integral_constant<int, 32>());
           fence_async_smem();
           tc_fence_after();
           issue_pv(sn, st, kt == 0);
@@ -656,44 +689,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
       const bool warp_ok = (r & ~31) < toks * G;  // (uniform: this warp has rows)
       const int pos_lo = it.ctx - it.qlen + it.tok0 + t * tpt;  // the tile's first position
       const int pos = row_ok ? pos_lo + tile_tok : -1;
-      const int masked = CAUSAL ? first_masked(it.ctx, it.qlen, it.tok0) : 0;
       float m_run = -INFINITY, l_run = 0.f;
       for (int k = 0; k < ntt; ++k, ++sn) {
         const int b = sn & 1, kt = it.t0 + k;
         if (!(ok = wwait(sm.s_full[t][b], (sn >> 1) & 1))) break;
         tc_fence_after();
-        const int rest = it.ctx - kt * kKeys;  // keys of this tile that the context holds, or more
-        if (rest < kKeys || (CAUSAL && kt >= masked)) {
-          // V of this tile without rows behind the context and without what is not finite where a row
-          // does not attend to it (by each warpgroup, whose P V follows: the second finds zeros, or
-          // writes the same ones)
-          const uint32_t x = num + k, st = x % kStages;
-          if (!(ok = wwait(sm.v_full[st], (x / kStages) & 1))) break;
-          if (rest < kKeys) {
-            const uint32_t from = smem_addr(sm.v[st]) + (r & 7) * 16;
-            for (int key = rest + (r >> 3); key < kKeys; key += 16)
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h) st_shared16(from + h * kHalf + key * 128, make_uint4(0, 0, 0, 0));
-          }
+        if (kTidySoftmax && untidy(it, kt)) {
+          const uint32_t x = num + k;
+          if (!(ok = wwait(sm.v_full[x % kStages], (x / kStages) & 1))) break;
+          tidy(it, j, kt, x % kStages, r, std::integral_constant<int, kRows>());
         }
-        if (CAUSAL && kt >= masked) {
-          const uint32_t st = (num + k) % kStages;
-          const uint32_t at = smem_addr(sm.v[st]) + r * 16;
-          uint32_t odd = 0;
-#pragma unroll
-          for (int c = 0; c < static_cast<int>(kStageBytes / 2048); ++c) {
-            if ((r >> 3) + (c & 3) * 16 >= rest) continue;  // (behind the context: zeros)
-            const uint4 w = ld_shared16(at + c * 2048);
-            odd |= odd_halves<T>(w.x) | odd_halves<T>(w.y) | odd_halves<T>(w.z) | odd_halves<T>(w.w);
-          }
-          if (odd) {
-            // (the flag first: who finds the zeros has to find it)
-            atomicOr(&sm.item[j % kItems].flags, kFlagOdd);
-            __threadfence_block();
-            clear_odd<T>(at, kStageBytes / 2048);
-          }
-        }
-        if (rest < kKeys || (CAUSAL && kt >= masked)) fence_async_smem();
         if (warp_ok) {
           float sv[kKeys];
           tmem_get64(tl + b * kColS, sv);
@@ -839,7 +844,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
             // the values of V that went in as zeros (rare: a later draft's row is not finite)
             T* row = outp + ((static_cast<size_t>(it.qs + it.tok0 + t * tpt + tile_tok) * p.num_q_heads) + it.g * G +
                              r - tile_tok * G) * D;
-            add_odd<D, T>(p, it.s, it.g, masked * kKeys, pos, 0, D, row);
+            add_odd<D, T>(p, it.s, it.g, first_masked(it.ctx, it.qlen, it.tok0) * kKeys, pos, 0, D, row);
           }
           __syncwarp();
         }
