@@ -891,32 +891,46 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
   const int tpt = p.tpt, G = p.group, tok = static_cast<int>((r * p.group_magic) >> 16);
   const int toks = min(tpt, j.end - (j.tok0 + t * tpt));
   if (tok >= toks) return;
-  int flags = 0;
-  // piece f: slot 1 of the first CTA, slot 0 of the others
-  auto slot = [&](int f) -> size_t { return f == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + f); };
-  const int at = t * kRows + r;
+  // piece f: slot 1 of the first CTA, slot 0 of the others; four loads under way together
+  const int pieces = j.followers + 1, at = t * kRows + r;
+  auto slot = [&](int f) -> size_t { return 2 * (blockIdx.x + f) + (f == 0 ? 1 : 0); };
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto sum_of = [&](int f) { return f < pieces ? p.sums[slot(f) * (NT * kRows) + at] : none; };
   float m = -INFINITY;
-  for (int f = 0; f <= j.followers; ++f) {
-    const float4 x = p.sums[slot(f) * (NT * kRows) + at];
-    flags |= __float_as_int(x.z);
-    if (x.y != 0.f) m = fmaxf(m, x.x);
+  int flags = 0;
+  for (int f0 = 0; f0 < pieces; f0 += 4) {
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = sum_of(f0 + k);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      flags |= __float_as_int(x[k].z);
+      if (x[k].y != 0.f) m = fmaxf(m, x[k].x);
+    }
   }
   float l = 0.f;
   float4 o[4] = {};
-#pragma unroll 2
-  for (int f = 0; f <= j.followers; ++f) {
-    const float4 x = p.sums[slot(f) * (NT * kRows) + at];
-    if (x.y == 0.f) continue;  // no key of the piece counts for this row: no O was written, or zeros
-    const float w = ex2(x.x - m);
-    l += x.y * w;
-    const float4* from = p.parts + slot(f) * (D / 4) * (NT * kRows) + at;
+  for (int f0 = 0; f0 < pieces; f0 += 2) {
+    float4 x[2], v[2][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = from[(c4 + c) * (NT * kRows)];
-      o[c].x += v.x * w;
-      o[c].y += v.y * w;
-      o[c].z += v.z * w;
-      o[c].w += v.w * w;
+    for (int k = 0; k < 2; ++k) {
+      x[k] = sum_of(f0 + k);
+      const float4* from = p.parts + slot(f0 + k) * (D / 4) * (NT * kRows) + at;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[k][c] = f0 + k < pieces ? from[(c4 + c) * (NT * kRows)] : none;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (x[k].y == 0.f) continue;  // no key of the piece counts for this row: no O was written, or zeros
+      const float w = ex2(x[k].x - m);
+      l += x[k].y * w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        o[c].x += v[k][c].x * w;
+        o[c].y += v[k][c].y * w;
+        o[c].z += v[k][c].z * w;
+        o[c].w += v[k][c].w * w;
+      }
     }
   }
   const float inv = 1.f / l;
