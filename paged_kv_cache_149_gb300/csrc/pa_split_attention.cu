@@ -17,18 +17,18 @@
 // cut into equal shares, one per SM, wherever the cut falls, so a launch is balanced whatever its
 // lengths are, and only items that a cut goes through are joined, by a second kernel.
 //
-// Design: one CTA per SM; every CTA finds its own share from the lengths (no host round trip, no
-// counter to reset, and the cuts depend on lengths alone: the same bits whatever the blocks'
-// places).  Its roles go from item to item at their own pace:
+// Design: one CTA per SM (two, of one query tile at head_dim 64); every CTA finds its own share from
+// the lengths (no host round trip, no counter to reset, and the cuts depend on lengths alone: the same bits
+// whatever the blocks' places).  Its roles go from item to item at their own pace:
 // * A query tile's rows are (token, query head of the kv head) pairs, 128 / G tokens x G heads.
 //   tcgen05 multiplies all 128 rows whatever their number: at 8 kv heads of 128 in bf16 that is
 //   65 K operations per key in the time in which an SM's share of HBM brings the key's 512
 //   bytes, 40 % of the tensor rate, so few rows still stream at the memory's rate; the softmax,
 //   which would not fit, runs in the warps that have rows only.
 // * Two loader warps bring 64-key tiles of K and V into a ring, whole blocks by TMA (128-byte
-//   swizzle), the ragged last block by 16-byte cp.async with zero fill, so no row past the context
-//   is read.  Block-table entries are looked up four tiles ahead.  K's warp also walks the share
-//   and announces its items; V's also brings q.
+//   swizzle).  What the last block holds behind the context is masked (K) or cleared in shared memory
+//   (V).  Table entries are looked up 32 blocks at once, a batch ahead.  K's warp also walks the
+//   share and announces its items.  A warp of its own brings q (of two query tiles, V's).
 // * An MMA warp per query tile: S = Q K^T into tensor memory (two buffers), O += P V with P read
 //   from tensor memory over the S it came from.  S of the next keys goes in before P V.
 // * A softmax warpgroup per query tile, one thread per row, keeps m and l; O is rescaled only when
@@ -39,6 +39,15 @@
 //   do attend to those keys get them added as they go out.
 // Every mbarrier wait is bounded (about 1 s) and checks a shared abort flag; after one that gave
 // up the CTA still waits, as long again at most, for its copies and MMAs in flight.
+//
+// On GB300, device time: 64 contexts of 128..2048 with up to seven drafts, 32 query / 8 kv heads of
+// 128, bf16, 55 us (285 MB, 5.2 TB/s); eight of 8..32 K with 5..16 rows 96 us (5.9 TB/s); 64 single rows
+// over 100..1500 states, 16 heads of 64, fp16, 49 us; 32 prompts of 3..448 rows over the same 48 us; 6 texts
+// of 900..2048 rows over 2000..8192 states, 32 / 8 heads, 460 us (1530 TFLOP/s).  With few rows a
+// 64-key tile is a chain of fixed latencies (scores read 215 cycles, maximum 250, weights 125, stored and
+// passed on 130, two waits of 100) against 690 (d = 64) or 1380 cycles of an SM's share of HBM: at d = 64
+// that chain bounds the launch, twice over where items are a dozen tiles long and each costs its start
+// and end.  Two CTAs an SM hide some of it (74 -> 51 us); of 128 they leave each a ring too short (98 -> 109).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -58,8 +67,11 @@ using namespace tc;
 constexpr int kRows = 128;      // rows of a query tile (MMA M, tensor-memory lanes)
 constexpr int kKeys = 64;       // keys of a K/V tile (MMA N of S, K of P V)
 constexpr int kItems = 4;       // items in flight between the roles
-constexpr int kItemCost = 2;    // an item's start and end, in key tiles, for the shares
-constexpr int kLeastPiece = 4;  // key tiles: a cut that would leave fewer moves to the item's end
+// An item's start and end, in key tiles, for the shares; and the least key tiles of a piece: a cut that
+// would leave fewer moves to the item's end.  (64 contexts of 128..2048 / 64 rows over 100..1500: 3 and 2
+// 54.9 / 48.6 us, 2 and 4 56.8 / 50.4, 1 and 2 59.5 / 53.9, 4 and 2 55.1 / 49.3.)
+constexpr int kItemCost = 3;
+constexpr int kLeastPiece = 2;
 constexpr int kMaxGrid = 1024;  // CTAs the workspace has descriptors for
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that forces a rescale of O
@@ -1042,7 +1054,8 @@ int split_attention_launch(const PrefillArgs& a, int num_tokens, bool causal, vo
   p.err = a.err;
   // no context that the tables can hold is long enough for two pieces: no join
   p.cut = static_cast<long long>(a.max_blocks_per_seq) * a.block_size > (2 * split::kLeastPiece - 1) * split::kKeys;
-  // two query tiles per item, which share each key tile's loads, where sequences have the rows
+  // Two query tiles per item, which share each key tile's loads, where sequences have the rows: 6 x 900..2048
+  // rows of four heads each 460 us.  With 119 rows a sequence one tile takes 48.8 us, two 54.
   const bool two = static_cast<long long>(num_tokens) * p.group > static_cast<long long>(split::kRows) * a.num_seqs;
   if (a.head_dim == 128)
     return a.bf16 ? split::launch2<128, __nv_bfloat16>(p, two, causal, sm_count, stream)

@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-ITEM_COST, LEAST_PIECE = 2, 4
+ITEM_COST, LEAST_PIECE = 3, 2
 
 
 def place(x, seqs, hkv, cut):
