@@ -237,7 +237,7 @@ def _pool_device(src, dst, *args, device=None, **kw):
 class Launch:
     """A library call whose arguments were checked and marshalled once (``plan=True`` on
     the decode step functions, decode_fp8_block, the prefills, reshape_and_cache,
-    append_fp8_block and build_step): ``run(stream)`` issues it again on ``stream`` over the
+    append_fp8_block, build_step, rotary, rotary_append, decode_drafts, cross and verify_drafts): ``run(stream)`` issues it again on ``stream`` over the
     same buffers, whose contents may change between runs.  For serving loops that launch
     the same step shape many times; the per-call cost is one foreign call.  The marshalled
     arguments are raw device addresses, so the Launch holds a reference to every tensor

@@ -341,3 +341,62 @@ def test_refusals():
         with pytest.raises(pa.PagedAttentionError):  # 129 query heads to a kv head
             call(p.q(2, 129).cuda(), kc, vc, t, c, s, 0.1,
                  workspace=torch.empty(1 << 26, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("block", [8, 16, 32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_contexts_up_to_the_tables_end(block, d):
+    """A full table, whose last entry is used, of lengths around every tile and block border."""
+    for c in (block, 63, 64, 65, 127, 128, 129, 191, 193, 320):
+        c = -(-c // block) * block
+        p = Paged([c, 1], 2, d, block, "bf16", seed=c)
+        p.tables = p.tables[:, :-1].contiguous()
+        p.width -= 1
+        q = p.q(3, 4)
+        for causal in (True, False):
+            out, err = run(pa.decode_drafts if causal else pa.cross, p, q, [0, 2, 3], p.ctx, 0.1)
+            assert err == 0
+            compare(out, p, q, [0, 2, 3], p.ctx, 0.1, causal)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (), generator=g))
+    n = pick(1, 40)
+    dtype, d, block = ("bf16", "fp16")[pick(0, 1)], (64, 128)[pick(0, 1)], (8, 16, 32)[pick(0, 2)]
+    hkv, G = pick(1, 4), (1, 2, 3, 4, 7, 8, 16)[pick(0, 6)]
+    top = (70, 600, 2500)[pick(0, 2)]
+    ctx = [pick(1, top) for _ in range(n)]
+    rows = [min(c, (pick(0, 4), pick(0, 40), pick(0, 200))[pick(0, 2)]) for c in ctx]
+    p = Paged(ctx, hkv, d, block, dtype, seed=seed)
+    qs = starts(rows)
+    if qs[-1] == 0:
+        return
+    q = p.q(qs[-1], G * hkv)
+    for causal in (True, False):
+        out, err = run(pa.decode_drafts if causal else pa.cross, p, q, qs, ctx, 1 / math.sqrt(d))
+        assert err == 0
+        compare(out, p, q, qs, ctx, 1 / math.sqrt(d), causal)
+
+
+def test_infinite_scores_and_values_that_are_attended_to():
+    """As the formula has it: a score of -inf is no weight, of +inf no number; an infinite value is infinite."""
+    p = Paged([300], 1, 64, 16, "bf16", seed=3)
+    p.k[0].fill_(1.0)
+    q = torch.ones(2, 1, 64, dtype=torch.bfloat16)
+    p.k[0][7] = -math.inf
+    out, _ = run(pa.cross, p, q, [0, 2], p.ctx, 0.125)
+    k = torch.cat([p.v[0][:7], p.v[0][8:]]).double().mean(0)
+    assert ((out.double() - k).abs() <= 3 * 2.0 ** -8 * p.v[0].double().abs().mean(0) + 2.0 ** -8 * k.abs()).all()
+    p.k[0].fill_(-math.inf)  # no key counts at all: 0 / 0
+    out, _ = run(pa.cross, p, q, [0, 2], p.ctx, 0.125)
+    assert out.isnan().all()
+    p.k[0].fill_(1.0)
+    p.k[0][200] = math.inf
+    out, _ = run(pa.cross, p, q, [0, 2], p.ctx, 0.125)
+    assert out.isnan().all()
+    p.k[0].fill_(1.0)
+    p.v[0][5, 0, 9] = math.inf
+    out, _ = run(pa.cross, p, q, [0, 2], p.ctx, 0.125)
+    assert (out[..., 9] == math.inf).all() and out[..., :9].isfinite().all() and out[..., 10:].isfinite().all()

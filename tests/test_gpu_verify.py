@@ -248,3 +248,60 @@ def test_refusals():
         pa.verify_drafts(tokens, torch.empty(3, 2 ** 20 + 1, device="cuda"), None, u, qs, ctx)
     empty = pa.verify_drafts(tokens[:0], p[:0], None, u[:0], i32([0, 0, 0]), i32([4, 5]))
     assert empty[1].tolist() == [0, 0] and empty[2].tolist() == [4, 5]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("pads,offsets", [((1, 2), (0, 0)), ((3, 3), (1, 3)), ((7, 16), (5, 0)), ((8, 8), (0, 1))])
+def test_rows_that_start_anywhere(dtype, pads, offsets):
+    """Target and draft rows at their own distances and places within 16 bytes."""
+    rows, V = [3, 1, 6, 2], 1003
+    tokens, p, q, u = make(rows, V, dtype, True, seed=17)
+    views = []
+    for t, pad, off in zip((p, q), pads, offsets):
+        flat = torch.full((t.shape[0] * (V + pad) + off,), math.nan, dtype=t.dtype)
+        view = flat[off:].view(t.shape[0], V + pad)[:, :V]
+        view.copy_(t)
+        views.append(flat.cuda()[off:].view(t.shape[0], V + pad)[:, :V])
+    qs = starts(rows)
+    for d in (views[1], None):
+        pa.get_device_error()
+        out, emitted, _ = pa.verify_drafts(tokens.cuda(), views[0], d, u.cuda(), i32(qs), i32([50] * 4))
+        assert pa.get_device_error() == 0
+        for s, r in enumerate(rows):
+            a, b = qs[s], qs[s + 1]
+            want, _ = verdict(tokens[a:b].tolist(), p[a:b], None if d is None else q[a:b], u[a:b])
+            assert out[a:b].tolist() == want + [-1] * (r - len(want)) and emitted[s] == len(want)
+
+
+def test_the_largest_vocabulary():
+    V = 2 ** 20
+    p = torch.zeros(2, V)
+    p[:, [0, 511, 512, 600000, V - 1]] = torch.tensor([0.125, 0.125, 0.25, 0.25, 0.25])
+    for u, want in ((0.0, 0), (0.125, 511), (0.25, 512), (0.5, 600000), (0.75, V - 1), (0.99, V - 1)):
+        out = pa.verify_drafts(i32([1, 2]), p.cuda(), None, torch.full((2,), u, device="cuda"), i32([0, 1, 2]), i32([1, 1]))[0]
+        assert out.tolist() == [want] * 2
+
+
+@pytest.mark.parametrize("n", [1, 77, 160, 400, 700])
+def test_batches_of_every_cluster_size(n):
+    """8, 4, 2 and 1 CTAs to a sequence give the same tokens."""
+    rows = [2] * n
+    tokens, p, q, u = make([2, 2, 2, 2], 900, "fp32", True, seed=23, extra=0)
+    rep = -(-n // 4)
+    check(rows, tokens.repeat(rep)[:2 * n], p.repeat(rep, 1)[:2 * n], q.repeat(rep, 1)[:2 * n], u.repeat(rep)[:2 * n])
+
+
+def test_two_streams_at_once():
+    rows = [3, 1, 4]
+    batches = [make(rows, 5000, "fp32", True, seed=s, extra=0) for s in (31, 32)]
+    qs, ctx = i32(starts(rows)), i32([20, 20, 20])
+    up = [[t.cuda() for t in b] for b in batches]
+    want = [pa.verify_drafts(*b, qs, ctx)[0].clone() for b in up]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(20):
+        for i in (0, 1):
+            got.append((i, pa.verify_drafts(*up[i], qs, ctx, stream=streams[i])[0]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i, t in got)
