@@ -1150,18 +1150,27 @@ def rotary_append(q, key, value, k_cache, v_cache, block_tables, context_lens, q
     k0, k1, k2 = key.stride()
     v0, v1, v2 = value.stride()
     o0, o1, o2 = out.stride()
+    i64 = T.i64
     if (q2 == k2 == v2 == o2 == 1 and q1 == k1 == v1 == o1 == d and ntok > 1 and key.dtype is dt
-            and value.dtype is dt and out.dtype is dt and key.get_device() == dev and value.get_device() == dev
-            and out.get_device() == dev):
-        rows = (q.data_ptr(), q0, key.data_ptr(), k0, value.data_ptr(), v0, out.data_ptr(), o0)
+            and value.dtype is dt and out.dtype is dt and k_cache.dtype is dt and v_cache.dtype is dt
+            and block_tables.dtype is i32 and context_lens.dtype is i32 and query_start.dtype is i32
+            and freqs.dtype is i64 and key.get_device() == dev and value.get_device() == dev
+            and out.get_device() == dev and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and block_tables.get_device() == dev and context_lens.get_device() == dev
+            and query_start.get_device() == dev and freqs.get_device() == dev
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and query_start.is_contiguous() and freqs.is_contiguous()):
+        args = (q.data_ptr(), q0, key.data_ptr(), k0, value.data_ptr(), v0, out.data_ptr(), o0,
+                k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
+                query_start.data_ptr(), freqs.data_ptr(), 2 * half, 1 if interleaved else 0, amplitude, n, ntok, nb, hq,
+                hkv, d, bs, _code16(dt))
     else:  # (one row, one head, or something to refuse)
-        rows = (*_rows_ptr(q, "q", hq, d, dt, dev), *_rows_ptr(key, "key", hkv, d, dt, dev),
-                *_rows_ptr(value, "value", hkv, d, dt, dev), *_rows_ptr(out, "out", hq, d, dt, dev))
-    args = (*rows, _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
-            _ptr(block_tables, "block_tables", i32, dev), width,
-            _ptr(context_lens, "context_lens", i32, dev), _ptr(query_start, "query_start", i32, dev),
-            _ptr(freqs, "freqs", T.i64, dev), 2 * half, 1 if interleaved else 0, amplitude, n, ntok, nb, hq, hkv, d, bs,
-            _code16(dt))
+        args = (*_rows_ptr(q, "q", hq, d, dt, dev), *_rows_ptr(key, "key", hkv, d, dt, dev),
+                *_rows_ptr(value, "value", hkv, d, dt, dev), *_rows_ptr(out, "out", hq, d, dt, dev),
+                _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+                _ptr(block_tables, "block_tables", i32, dev), width, _ptr(context_lens, "context_lens", i32, dev),
+                _ptr(query_start, "query_start", i32, dev), _ptr(freqs, "freqs", i64, dev), 2 * half,
+                1 if interleaved else 0, amplitude, n, ntok, nb, hq, hkv, d, bs, _code16(dt))
     if plan:
         return Launch("pa_rotary_append", args, out,
                       keep=(q, key, value, k_cache, v_cache, block_tables, context_lens, query_start, freqs))
