@@ -502,7 +502,8 @@ size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
  *   where all of them are zero, target[a].  With every draft accepted, a = q_s - 1: target[a].
  *   The sampled token is the smallest t whose running sum of weights exceeds
  *   uniforms[q_s - 1] times their sum.  Sums are exact in units of 2^-54: the token depends on no
- *   order of addition.
+ *   order of addition.  (Numbers outside [0, 1): below 0 and NaN sample as 0, 1 and more the last
+ *   token that has a weight.)
  * out_tokens [num_tokens]: rows 0 .. a - 1 the accepted drafts, row a the sampled token, -1 behind
  * it.  emitted[s] = a + 1.  context_next[s] = context_lens[s] - q_s + emitted[s]: the tokens whose
  * K/V rows stay (context_lens count the step's tokens; the next step adds its own); it may be
