@@ -252,3 +252,32 @@ def test_refusals():
         call(q=off)
     none = b.q[:0]
     assert pa.rotary(none, b.k[:0], ctx, qs, freqs)[0].shape == (0, 2, 64)
+
+
+def test_rows_that_belong_to_no_sequence():
+    b = Batch([3, 1], [5, 0], 4, 2, 64, 16, "bf16", True, extra=6)
+    freqs, _ = pa.rotary_frequencies(64)
+    q0 = b.q.clone()
+    pa.get_device_error()
+    pa.rotary(b.q, b.k, i32([8, 1]), i32([2, 5, 6]), freqs, out=b.q, key_out=b.k)
+    assert pa.get_device_error() == 0
+    assert torch.equal(b.q[[0, 1, 6, 7, 8, 9]], q0[[0, 1, 6, 7, 8, 9]])
+    pos = torch.tensor([5, 6, 7, 0])
+    close(b.q[2:6].cpu(), *turned64(q0[2:6].cpu(), pos, angles64(64, 10000.0), False, 1.0), b.dt)
+    q1 = b.q.clone()
+    pa.rotary(b.q, b.k, i32([8, 1]), i32([0, 0, 0]), freqs, out=b.q, key_out=b.k)
+    assert torch.equal(b.q, q1)
+
+
+def test_two_streams_at_once():
+    batches = [Batch([40, 1, 7], [5, 100, 0], 8, 2, 128, 16, "bf16", True, seed=s) for s in (1, 2)]
+    freqs, _ = pa.rotary_frequencies(128)
+    args = [(b.q, b.k, b.v, b.kc, b.vc, b.tables.cuda(), i32(b.ctx), i32(b.qs), freqs) for b in batches]
+    want = [pa.rotary_append(*a).clone() for a in args]
+    caches = [b.kc.clone() for b in batches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [(i, pa.rotary_append(*args[i], stream=streams[i])) for _ in range(20) for i in (0, 1)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[:batches[i].n], want[i][:batches[i].n]) for i, o in got)
+    assert all(torch.equal(b.kc, c) for b, c in zip(batches, caches))

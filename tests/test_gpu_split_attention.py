@@ -400,3 +400,31 @@ def test_infinite_scores_and_values_that_are_attended_to():
     p.v[0][5, 0, 9] = math.inf
     out, _ = run(pa.cross, p, q, [0, 2], p.ctx, 0.125)
     assert (out[..., 9] == math.inf).all() and out[..., :9].isfinite().all() and out[..., 10:].isfinite().all()
+
+
+@pytest.mark.parametrize("ctx,rows", [([1500], [1500]), ([3000, 70], [2500, 70]), ([700] * 4, [700, 699, 1, 350])])
+def test_prompts_from_scratch(ctx, rows):
+    """Pieces of keys that come after every row of their query tile: nothing to add."""
+    for dtype, hq, hkv, d in (("bf16", 4, 1, 128), ("fp16", 2, 2, 64)):
+        p = Paged(ctx, hkv, d, 16, dtype, seed=13)
+        qs = starts(rows)
+        q = p.q(qs[-1], hq)
+        out, err = run(pa.decode_drafts, p, q, qs, ctx, 0.1)
+        assert err == 0
+        compare(out, p, q, qs, ctx, 0.1, True)
+
+
+def test_rows_that_belong_to_no_sequence():
+    p = Paged([300, 40], 1, 64, 16, "bf16", seed=4)
+    q = p.q(9, 2)
+    for call in (pa.decode_drafts, pa.cross):
+        out = torch.full_like(q, 7.0).cuda()
+        out, err = run(call, p, q, [0, 0, 0], p.ctx, 0.125, out=out)  # nobody has rows
+        assert err == 0 and (out == 7.0).all()
+        out = torch.full_like(q, 7.0).cuda()
+        out, err = run(call, p, q, [2, 5, 6], p.ctx, 0.125, out=out)  # the first two and the last three
+        assert err == 0 and (out[[0, 1, 6, 7, 8]] == 7.0).all()
+        for s, (a, b) in enumerate(((2, 5), (5, 6))):
+            first = p.ctx[s] - (b - a) if call is pa.decode_drafts else None
+            ref, mass = attend64(q[a:b], p.k[s], p.v[s], 0.125, first)
+            assert ((out[a:b].double() - ref).abs() <= attention_tolerance(ref, mass, p.dt, 64)).all()
