@@ -89,29 +89,26 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       xb[k] = source(u)[b];
     }
   }
-  // the row's sequence: the number of spans that end at or before it
-  int ended = 0;
+  // the row's sequence: the first one with a possible span that holds it.  (Counting the spans that end at or
+  // before it reads half as much, but beside a decreasing span finds one that does not hold it.)
+  int found = p.num_seqs;
   bool wrong = false;
   for (int s = tid; s < p.num_seqs; s += kThreads) {
-    const int qe = p.query_start[s + 1];
-    ended += qe <= tok;
-    if (tok == 0) {  // (one CTA tells of impossible spans)
-      const int qs = p.query_start[s];
-      wrong = wrong || qs < 0 || qe < qs || qe > p.num_tokens;
-    }
+    const int qs = p.query_start[s], qe = p.query_start[s + 1];
+    const bool span = qs >= 0 && qe >= qs && qe <= p.num_tokens;
+    if (span && qs <= tok && tok < qe) found = min(found, s);
+    wrong = wrong || !span;
   }
-  if (wrong) atomicOr(p.err, kErrBadContext);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ended += __shfl_xor_sync(0xffffffffu, ended, o);
+  if (wrong && tok == 0) atomicOr(p.err, kErrBadContext);  // (one CTA tells of impossible spans)
+  found = __reduce_min_sync(0xffffffffu, found);
   __shared__ int part[kThreads / 32];
-  if ((tid & 31) == 0) part[tid >> 5] = ended;
+  if ((tid & 31) == 0) part[tid >> 5] = found;
   __syncthreads();
-  int s = 0;
+  int s = p.num_seqs;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += part[w];
-  if (s >= p.num_seqs) return;  // behind the last sequence
+  for (int w = 0; w < kThreads / 32; ++w) s = min(s, part[w]);
+  if (s >= p.num_seqs) return;  // of no sequence
   const int qs = p.query_start[s], qe = p.query_start[s + 1], ctx = p.context_lens[s];
-  if (qs < 0 || qs > tok || qe > p.num_tokens) return;  // (an impossible span, told of above)
   const long long cap = CACHE ? static_cast<long long>(p.max_blocks_per_seq) << p.log2_block : 0x7fffffffll;
   if (qe - qs > ctx || ctx > cap) {
     if (tid == 0) atomicOr(p.err, kErrBadContext);

@@ -281,3 +281,34 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(o[:batches[i].n], want[i][:batches[i].n]) for i, o in got)
     assert all(torch.equal(b.kc, c) for b, c in zip(batches, caches))
+
+
+@pytest.mark.parametrize("qs, written", [
+    ([0, 8, 2, 4, 6], [0, 1, 2, 3, 4, 5, 6, 7]),  # sequence 1 decreases: every row is sequence 0's
+    ([0, 30, 2, 4, 6], [2, 3, 4, 5]),              # rows 6 and 7 are behind every span
+    ([0, -3, 2, 4, 6], [2, 3, 4, 5]),
+    ([6, 8, 1, 3, 3], [1, 2, 6, 7]),
+])
+def test_rows_beside_impossible_spans(qs, written):
+    # contexts that fill the tables: a row taken for a place behind its sequence's last would be past them
+    b = Batch([2, 2, 2, 2], [5, 5, 5, 5], 2, 1, 64, 16, "bf16", False, extra=0)
+    freqs, _ = pa.rotary_frequencies(64)
+    tables = torch.arange(4, dtype=torch.int32).reshape(4, 1)
+    kc, vc = (torch.zeros(4, 1, 16, 64, dtype=b.dt, device="cuda") for _ in range(2))
+    out = torch.full_like(b.q, 7.0)
+    pa.get_device_error()
+    pa.rotary_append(b.q, b.k, b.v, kc, vc, tables.cuda(), i32([16] * 4), i32(qs), freqs, out=out)
+    assert pa.get_device_error() == pa.DEVERR_BAD_CONTEXT
+    assert (out != 7.0).flatten(1).any(1).nonzero().flatten().tolist() == written
+    # each row in the slot of the sequence that holds it, and no other slot
+    slots = {}
+    for r in written:
+        s = next(s for s in range(4) if 0 <= qs[s] <= r < qs[s + 1] <= 8)
+        slots[(s, 16 - qs[s + 1] + r)] = r
+    want = torch.zeros_like(vc)
+    for (s, row), r in slots.items():
+        want[s, 0, row] = b.v[r, 0]
+    assert torch.equal(vc, want)
+    other = torch.full_like(b.q, 7.0)
+    pa.rotary(b.q, b.k, i32([16] * 4), i32(qs), freqs, out=other, key_out=torch.empty_like(b.k))
+    assert pa.get_device_error() == pa.DEVERR_BAD_CONTEXT and torch.equal(other, out)
