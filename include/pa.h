@@ -497,12 +497,13 @@ size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
  * alike), in [0, 1] (what is negative or no number counts as 0, above 1 as 1); a row need not sum
  * to 1.  uniforms [num_tokens] float32 in [0, 1).
  *   Draft i + 1 is accepted while uniforms[i] * draft[i][x] < target[i][x], x = tokens[i + 1] (rows of
- *   the sequence; draft 1 where NULL).  A token outside [0, V) is refused.
+ *   the sequence; draft 1 where NULL; probabilities as they count, and uniforms[i] alike: below 0 and
+ *   NaN as 0, above 1 as 1).  A token outside [0, V) is refused.
  *   At the first refusal, row a: weights max(target[a] - draft[a], 0) (NULL: target[a] without x);
  *   where all of them are zero, target[a].  With every draft accepted, a = q_s - 1: target[a].
  *   The sampled token is the smallest t whose running sum of weights exceeds
  *   uniforms[q_s - 1] times their sum.  Sums are exact in units of 2^-54: the token depends on no
- *   order of addition.  (Numbers outside [0, 1): below 0 and NaN sample as 0, 1 and more the last
+ *   order of addition.  (A number outside [0, 1): below 0 and NaN sample as 0, 1 and more the last
  *   token that has a weight.)
  * out_tokens [num_tokens]: rows 0 .. a - 1 the accepted drafts, row a the sampled token, -1 behind
  * it.  emitted[s] = a + 1.  context_next[s] = context_lens[s] - q_s + emitted[s]: the tokens whose

@@ -1285,11 +1285,12 @@ def verify_drafts(tokens, target_probs, draft_probs, uniforms, query_start, cont
     certain; uniforms [num_tokens] float32 in [0, 1).  A draft x in row i + 1 is accepted while
     uniforms[i] * draft[i, x] < target[i, x]; then a token is drawn from max(target - draft, 0) of
     the first row refused, or from the last row's target, by inversion with the sequence's last
-    uniform.  Returns (out [num_tokens]: accepted drafts, the drawn token, -1; emitted [num_seqs]:
-    tokens that came out; context_next [num_seqs]: context_lens - q_len + emitted, the tokens
-    whose K/V rows stay, which may be context_lens itself).  Rows of the probabilities may lie
-    farther apart than vocab.  plan=True returns a Launch whose runs return out (emitted and
-    context_next must then be given)."""
+    uniform.  Probabilities and uniforms below 0 and NaN count as 0, above 1 as 1.  Returns (out
+    [num_tokens]: accepted drafts, the drawn token, -1; emitted [num_seqs]: tokens that came out;
+    context_next [num_seqs]: context_lens - q_len + emitted, the tokens whose K/V rows stay, which
+    may be context_lens itself).  Rows of the probabilities may lie farther apart than vocab.
+    plan=True returns a Launch whose runs return out (emitted and context_next must then be
+    given)."""
     T = _T or _torch()
     dev, i32 = _device_of(tokens, "tokens"), T.i32
     ntok, = tokens.shape

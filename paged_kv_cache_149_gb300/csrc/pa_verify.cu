@@ -106,7 +106,8 @@ struct Parts {
   }
 };
 
-// A probability as it counts: what is no number or negative as 0, above 1 as 1.
+// A probability, or a uniform number in a draft's test, as it counts: what is no number or negative as
+// 0, above 1 as 1.
 __device__ __forceinline__ float counted(float x) { return __saturatef(x); }
 
 // A row of probabilities, read in 16-byte pieces of VE values.  `skew`: values between the aligned
@@ -203,9 +204,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     const int x = p.tokens[qs + i + 1];
     bool good = false;
     if (x >= 0 && x < p.vocab) {
-      const float pt = value(target + i * p.target_stride + x);
-      const float dt = draft ? value(draft + i * p.draft_stride + x) : 1.f;
-      good = static_cast<double>(p.uniforms[qs + i]) * static_cast<double>(dt) < static_cast<double>(pt);
+      // (as they count in the sums; the uniform number too: raw, a negative draft probability took in a
+      // token that the target gives none)
+      const float pt = counted(value(target + i * p.target_stride + x));
+      const float dt = draft ? counted(value(draft + i * p.draft_stride + x)) : 1.f;
+      good = static_cast<double>(counted(p.uniforms[qs + i])) * static_cast<double>(dt) < static_cast<double>(pt);
     }
     if (!good) {
       atomicMin(&sm.refused, i);
