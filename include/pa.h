@@ -72,7 +72,7 @@ enum {
 #define PA_DEVERR_TIMEOUT     0x10u /* a bounded wait gave up (about 1 s; prefill pipeline, decode
                                          split-KV merge): output invalid */
 #define PA_DEVERR_NO_BLOCKS   0x20u /* build_step: fewer free blocks than the step needs */
-#define PA_DEVERR_BAD_PROBS   0x40u /* verify_drafts: a row of probabilities without a positive one */
+#define PA_DEVERR_BAD_PROBS   0x40u /* verify_drafts: a row of probabilities none of which is above 2^-55 */
 
 /*
  * pa_reshape_and_cache -- write each new token's K and V rows into its cache slot.
@@ -502,14 +502,16 @@ size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
  *   At the first refusal, row a: weights max(target[a] - draft[a], 0) (NULL: target[a] without x);
  *   where all of them are zero, target[a].  With every draft accepted, a = q_s - 1: target[a].
  *   The sampled token is the smallest t whose running sum of weights exceeds
- *   uniforms[q_s - 1] times their sum.  Sums are exact in units of 2^-54: the token depends on no
+ *   uniforms[q_s - 1] times their sum.  For weights and sums, target and draft values are whole
+ *   units of 2^-54, each rounded to nearest (from 2^-31 on fp32 loses nothing; 2^-55 and less is 0, so a row
+ *   or a rest of nothing but such values counts as all zero), and sums are exact: the token depends on no
  *   order of addition.  (A number outside [0, 1): below 0 and NaN sample as 0, 1 and more the last
  *   token that has a weight.)
  * out_tokens [num_tokens]: rows 0 .. a - 1 the accepted drafts, row a the sampled token, -1 behind
  * it.  emitted[s] = a + 1.  context_next[s] = context_lens[s] - q_s + emitted[s]: the tokens whose
  * K/V rows stay (context_lens count the step's tokens; the next step adds its own); it may be
- * context_lens itself.  A sequence without rows: 0 and context_lens[s].  A row a without a positive probability: -1 there,
- * emitted[s] = a, PA_DEVERR_BAD_PROBS.  context_lens[s] < q_s: 0, context_lens[s],
+ * context_lens itself.  A sequence without rows: 0 and context_lens[s].  A row a without a probability
+ * above 2^-55: -1 there, emitted[s] = a, PA_DEVERR_BAD_PROBS.  context_lens[s] < q_s: 0, context_lens[s],
  * PA_DEVERR_BAD_CONTEXT.  V <= 2^20; out_tokens must not be tokens.  The launch lets none after it
  * start early, so the lengths it writes may be read by any call that follows it in the stream.
  * Blocks that a rejected draft had opened stay in the request's table (every call reads
