@@ -454,8 +454,9 @@ int pa_rotary(const void* q, int64_t q_stride, const void* key, int64_t key_stri
  * q, out [num_tokens][Hq][d]; row i of sequence s is at position context_lens[s] - q_s + i, attends
  * to positions up to its own, and its K/V rows are already in the cache (pa_rotary_append).
  * scale > 0; Hq / Hkv <= 128; Hq <= 65536.  Accumulation fp32; fp16 weights keep what is above 2^-31
- * of a row's largest.  V may hold magnitudes up to 2^100.  A key that a row does not attend to
- * changes none of its bits, whatever it holds, NaN and infinities among it.
+ * of a row's largest.  Scores, scaled or not, may be of any size that fp32 holds (a row's largest has the
+ * weight 1).  V may hold magnitudes up to 2^100.  A key that a row does not attend to changes none
+ * of its bits, whatever it holds, NaN and infinities among it.
  * The cuts depend on query_start, context_lens, max_blocks_per_seq, num_tokens and the head shape
  * alone, never on where blocks sit.
  * A sequence with rows and an invalid context (ctx < 1, ctx > T * B, q_s > ctx) gets zeros and

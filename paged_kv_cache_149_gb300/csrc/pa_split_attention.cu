@@ -4,7 +4,7 @@
 //
 // Row i of sequence s (q_len rows, context c) attends to t <= c - q_len + i, or to all t < c:
 //   out = sum_t softmax_t(scale <q, K_t>) V_t
-// Over a cut of the keys into pieces j, with m_j the largest scaled score of a piece (in log2
+// Over a cut of the keys into pieces j, with m_j about the largest scaled score of a piece (in log2
 // units), l_j = sum 2^(z_t - m_j) and O_j = sum 2^(z_t - m_j) V_t:
 //   m = max_j m_j,   out = sum_j 2^(m_j - m) O_j / sum_j 2^(m_j - m) l_j
 // which is exact, so a cut costs one fp32 rounding and no accuracy worth the name.
@@ -75,6 +75,11 @@ constexpr int kLeastPiece = 2;
 constexpr int kMaxGrid = 1024;  // CTAs the workspace has descriptors for
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that forces a rescale of O
+// Rows whose maximum is this far from zero (log2 units) have it taken off their scores before these are scaled
+// (far_tiles).  Else a weight is one multiply-add of the score, relative to the scaled maximum rounded to fp32: half a
+// step of it is 2^-12 at 2^12 (all of a row's weights share it), but past 2^24 a whole power of two and more, with which
+// the largest weight leaves f16's or even fp32's range (scores of 4e8 in f16 came out as infinity or 0 / 0).
+constexpr float kFar = 4096.f;
 // P = 2^(z - m + lift) <= 2^15 in f16, whose smallest value is 2^-24: lift 7; bf16 needs none.
 template <typename T>
 __host__ __device__ constexpr float lift_of() { return std::is_same<T, __half>::value ? 7.f : 0.f; }
@@ -101,7 +106,7 @@ struct Params {
   const int32_t* query_start;  // [n + 1]
   uint8_t* out;
   Join* joins;    // [grid]
-  float4* sums;   // [grid][2][query tiles * kRows] (m, l, flags) of a cut item's rows
+  float4* sums;   // [grid][2][query tiles * kRows] (m, l, flags, base) of a cut item's rows
   float4* parts;  // [grid][2][d / 4][query tiles * kRows] their O, row fastest
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group, tpt;  // tpt = tokens per query tile
   int max_blocks_per_seq, block_size, log2_block, num_blocks;
@@ -230,6 +235,141 @@ __device__ __forceinline__ void add_odd(const Params& p, int s, int g, int first
       if (!(fabsf(x) < INFINITY)) out[i] = from_float<T>(static_cast<float>(out[i]) + x);
     }
   }
+}
+
+// V of a key tile (in stage st, of item j) for P V, by kAll threads: keys from `rest` on, behind the context, become
+// zeros, and so do, where not every row attends to all of the tile, values that are not finite.
+template <int D, typename T, int NT, bool CAUSAL, int kAll>
+__device__ __forceinline__ void tidy_tile(Smem<D, NT>& sm, int rest, bool masked, int j, uint32_t st, int me) {
+  constexpr uint32_t kHalf = kKeys * 128, kStageBytes = kKeys * D * 2;
+  const uint32_t v = smem_addr(sm.v[st]);
+#pragma unroll 1
+  for (int key = max(rest, 0) + (me >> 3); key < kKeys; key += kAll / 8)
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+      st_shared16(v + (me & 7) * 16 + h * kHalf + key * 128, make_uint4(0, 0, 0, 0));
+  if (CAUSAL && masked) {
+    const uint32_t at = v + me * 16;
+    uint32_t odd = 0;
+#pragma unroll 4
+    for (int c = 0; c < static_cast<int>(kStageBytes / 16 / kAll); ++c) {
+      if ((me + c * kAll) % (kHalf / 16) / 8 >= rest) continue;  // (behind the context: zeros)
+      const uint4 w = ld_shared16(at + c * kAll * 16);
+      odd |= odd_halves<T>(w.x) | odd_halves<T>(w.y) | odd_halves<T>(w.z) | odd_halves<T>(w.w);
+    }
+    if (odd) {
+      // (the flag first: who finds the zeros has to find it)
+      atomicOr(&sm.item[j % kItems].flags, kFlagOdd);
+      __threadfence_block();
+      auto clean = [](uint32_t x) -> uint32_t { return x & ~((odd_halves<T>(x) >> 15) * 0xffffu); };
+#pragma unroll 1
+      for (int c = 0; c < static_cast<int>(kStageBytes / 16 / kAll); ++c) {
+        const uint4 w = ld_shared16(at + c * kAll * 16);
+        st_shared16(at + c * kAll * 16, make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w)));
+      }
+    }
+  }
+  fence_async_smem();
+  __syncwarp();
+}
+
+// What the softmax keeps of a row: its weights are relative to base * scale + m in log2 units.
+struct RowState {
+  float m, l, base;
+  int ok;  // no wait gave up
+};
+
+// A warp's softmax over an item's key tiles k .. ntt - 1 where a row's maximum is far from zero.  A maximum that grows
+// becomes the row's base, a score, which is taken off the others before they are scaled.  S of tile k has been waited for,
+// its V is tidy, and O is relative to f.m; `last` is the last key that this row attends to.  A function that is not
+// inlined: with this in the loop of near rows, in any of six forms, that loop lost 2 to 10 % to registers.
+template <int D, typename T, int NT, bool CAUSAL>
+__device__ __noinline__ RowState far_tiles(Smem<D, NT>* smp, unsigned* err, float scale_log2, RowState f, int k, int ntt,
+                                           uint32_t sn, uint32_t num, int t0, int ctx, int qlen, int tok0, int j,
+                                           uint32_t tl, int t, int last) {
+  Smem<D, NT>& sm = *smp;
+  constexpr int kStages = Shape<D, NT>::kStages;
+  constexpr uint32_t kColS = kKeys, kColO = 2 * kKeys;
+  const int r = threadIdx.x & (kRows - 1), lane = threadIdx.x & 31;
+  auto wwait = [&](unsigned long long& bar, uint32_t parity) -> bool {
+    const bool done = mbar_wait_bounded(smem_addr(&bar), parity, &sm.abort);
+    if (!done && atomicExch(&sm.abort, 1) == 0) atomicOr(err, kErrTimeout);
+    return __all_sync(0xffffffffu, done) != 0;
+  };
+  f.ok = 0;
+  for (bool first = true; k < ntt; first = false, ++k, ++sn) {
+    const int b = sn & 1, kt = t0 + k;
+    if (!first) {
+      if (!wwait(sm.s_full[t][b], (sn >> 1) & 1)) return f;
+      tc_fence_after();
+      const bool masked = CAUSAL && kt >= first_masked(ctx, qlen, tok0);
+      if (NT == 1 && (ctx - kt * kKeys < kKeys || masked)) {
+        const uint32_t x = num + k;
+        if (!wwait(sm.v_full[x % kStages], (x / kStages) & 1)) return f;
+        tidy_tile<D, T, NT, CAUSAL, kRows>(sm, ctx - kt * kKeys, masked, j, x % kStages, r);
+      }
+    }
+    const int lim = last < 0 ? -1 : last - kt * kKeys;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float x[32];
+      tmem_get32(tl + b * kColS + 32 * h, x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * h + i <= lim) top = fmaxf(top, x[i]);
+    }
+    const float mx = (top - f.base) * scale_log2;
+    bool need = f.m == -INFINITY ? top > -INFINITY : mx > f.m + kRescale;
+    if (first && top > -INFINITY && f.m == mx) {  // (taken up, and O rescaled, before the call)
+      f.base = top;
+      f.m = 0.f;
+      need = false;
+    }
+    if (__any_sync(0xffffffffu, need)) {
+      float alpha = 1.f;
+      if (need) {
+        alpha = f.m == -INFINITY ? 0.f : ex2(f.m - mx);
+        f.l *= alpha;
+        f.base = top;
+        f.m = 0.f;
+      }
+      if (k > 0) {
+        if (!wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1)) return f;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          tmem_get32(tl + kColO + c0, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          tmem_st32(tl + kColO + c0, o);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
+    }
+    const float off = (f.m == -INFINITY ? 0.f : -f.m) + lift_of<T>();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float x[32];
+      uint32_t pk[16];
+      tmem_get32(tl + b * kColS + 32 * h, x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        x[i] = 32 * h + i <= lim ? ex2(fmaf(x[i] - f.base, scale_log2, off)) : 0.f;
+        f.l += x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+      tmem_st16(tl + b * kColS + 16 * h, pk);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[t][b]));
+  }
+  f.ok = 1;
+  return f;
 }
 
 template <int D, typename T, int NT, bool CAUSAL>
@@ -453,37 +593,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
     return it.ctx - kt * kKeys < kKeys || (CAUSAL && kt >= first_masked(it.ctx, it.qlen, it.tok0));
   };
   auto tidy = [&](const Item& it, int j, int kt, uint32_t st, int me, auto all) {
-    constexpr int kAll = decltype(all)::value;  // threads that share the work
-    const int rest = it.ctx - kt * kKeys;       // keys of this tile that the context holds, or more
-    const uint32_t v = smem_addr(sm.v[st]);
-#pragma unroll 1
-    for (int key = max(rest, 0) + (me >> 3); key < kKeys; key += kAll / 8)
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        st_shared16(v + (me & 7) * 16 + h * kHalf + key * 128, make_uint4(0, 0, 0, 0));
-    if (CAUSAL && kt >= first_masked(it.ctx, it.qlen, it.tok0)) {
-      const uint32_t at = v + me * 16;
-      uint32_t odd = 0;
-#pragma unroll 4
-      for (int c = 0; c < static_cast<int>(kStageBytes / 16 / kAll); ++c) {
-        if ((me + c * kAll) % (kHalf / 16) / 8 >= rest) continue;  // (behind the context: zeros)
-        const uint4 w = ld_shared16(at + c * kAll * 16);
-        odd |= odd_halves<T>(w.x) | odd_halves<T>(w.y) | odd_halves<T>(w.z) | odd_halves<T>(w.w);
-      }
-      if (odd) {
-        // (the flag first: who finds the zeros has to find it)
-        atomicOr(&sm.item[j % kItems].flags, kFlagOdd);
-        __threadfence_block();
-        auto clean = [](uint32_t x) -> uint32_t { return x & ~((odd_halves<T>(x) >> 15) * 0xffffu); };
-#pragma unroll 1
-        for (int c = 0; c < static_cast<int>(kStageBytes / 16 / kAll); ++c) {
-          const uint4 w = ld_shared16(at + c * kAll * 16);
-          st_shared16(at + c * kAll * 16, make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w)));
-        }
-      }
-    }
-    fence_async_smem();
-    __syncwarp();
+    tidy_tile<D, T, NT, CAUSAL, decltype(all)::value>(
+        sm, it.ctx - kt * kKeys, kt >= first_masked(it.ctx, it.qlen, it.tok0), j, st, me);
   };
   // The item's key tiles end here for its query tiles together.
   auto item_end = [&](const Item& it, int* e0, int* e1) -> int {
@@ -707,7 +818,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
       const int pos_lo = it.ctx - it.qlen + it.tok0 + t * tpt;  // the tile's first position
       const int pos = row_ok ? pos_lo + tile_tok : -1;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int k = 0; k < ntt; ++k, ++sn) {
+      int k = 0;
+      for (; k < ntt; ++k, ++sn) {
         const int b = sn & 1, kt = it.t0 + k;
         if (!(ok = wwait(sm.s_full[t][b], (sn >> 1) & 1))) break;
         tc_fence_after();
@@ -735,22 +847,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
           for (int i = 8; i < kKeys; i += 8)
 #pragma unroll
             for (int c = 0; c < 4; ++c) pm[c] = fmax3(pm[c], sv[i + 2 * c], sv[i + 2 * c + 1]);
-          const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
-          if (k == 0) {
-            m_run = mx;
-          } else {
-            const bool need = row_ok && mx > m_run + kRescale;
-            if (__any_sync(0xffffffffu, need)) {
+          const float top = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mx = top * p.scale_log2;
+          // (an item's first maximum grows from -inf)
+          const bool need = row_ok && mx > m_run + kRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            float alpha = 1.f;
+            if (need) {
+              alpha = ex2(m_run - mx);
+              l_run *= alpha;
+              m_run = mx;
+            }
+            if (k > 0) {
               // rescale O, once P V of the tile before is done (the one before that was issued
               // before this S)
               if (!(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
               tc_fence_after();
-              float alpha = 1.f;
-              if (need) {
-                alpha = ex2(m_run - mx);
-                l_run *= alpha;
-                m_run = mx;
-              }
 #pragma unroll
               for (int c0 = 0; c0 < D; c0 += 32) {
                 float o[32];
@@ -761,6 +872,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
               }
               asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
+            // far from zero: far_tiles does the rest of the item
+            if (__any_sync(0xffffffffu, row_ok && fabsf(m_run) >= kFar && top > -INFINITY)) break;
           }
           // P over this thread's own row of S, already in registers, rounded to the input type; its
           // unrounded sum in l (a row with every score at -inf so far: any finite offset gives 0)
@@ -788,6 +901,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[t][b]));
       }
+      float base = 0.f;
+      if (ok && k < ntt) {
+        const RowState f = far_tiles<D, T, NT, CAUSAL>(&sm, p.err, p.scale_log2, RowState{m_run, l_run, 0.f, 1}, k, ntt, sn,
+                                                       num, it.t0, it.ctx, it.qlen, it.tok0, j, tl, t,
+                                                       row_ok ? (CAUSAL ? pos : it.ctx - 1) : -1);
+        m_run = f.m;
+        l_run = f.l;
+        base = f.base;
+        ok = f.ok;
+        sn += ntt - k;
+      }
       if (!ok) break;
       if (ntt > 0 && !(ok = wwait(sm.pv_done[t][(sn - 1) & 1], ((sn - 1) >> 1) & 1))) break;
       tc_fence_after();
@@ -799,7 +923,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
         // ---- a piece: m, l and O for the join, row fastest: a warp's store is 512 bytes ----
         const size_t row0 = static_cast<size_t>(it.slot) * (NT * kRows) + t * kRows + r;
         if (warp_ok) {
-          p.sums[row0] = make_float4(m_run, l_run, __int_as_float((bad ? kFlagBad : 0) | (flags & kFlagOdd)), 0.f);
+          p.sums[row0] = make_float4(m_run, l_run, __int_as_float((bad ? kFlagBad : 0) | (flags & kFlagOdd)), base);
           if (ntt > 0) {
             float4* to = p.parts + static_cast<size_t>(it.slot) * (D / 4) * (NT * kRows) + t * kRows + r;
 #pragma unroll
@@ -913,7 +1037,9 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
   auto slot = [&](int f) -> size_t { return 2 * (blockIdx.x + f) + (f == 0 ? 1 : 0); };
   const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
   auto sum_of = [&](int f) { return f < pieces ? p.sums[slot(f) * (NT * kRows) + at] : none; };
-  float m = -INFINITY;
+  // the largest reference, as (m, base); log2 of a piece's weight over its
+  float m = -INFINITY, base = 0.f;
+  auto above = [&](const float4& x) { return (x.w - base) * p.scale_log2 + (x.x - m); };
   int flags = 0;
   for (int f0 = 0; f0 < pieces; f0 += 4) {
     float4 x[4];
@@ -922,7 +1048,10 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       flags |= __float_as_int(x[k].z);
-      if (x[k].y != 0.f) m = fmaxf(m, x[k].x);
+      if (x[k].y != 0.f && (m == -INFINITY || above(x[k]) > 0.f)) {
+        m = x[k].x;
+        base = x[k].w;
+      }
     }
   }
   float l = 0.f;
@@ -939,7 +1068,7 @@ __global__ void __launch_bounds__(kRows) join_kernel(const __grid_constant__ Par
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (x[k].y == 0.f) continue;  // no key of the piece counts for this row: no O was written, or zeros
-      const float w = ex2(x[k].x - m);
+      const float w = ex2(above(x[k]));
       l += x[k].y * w;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
