@@ -511,9 +511,10 @@ size_t pa_split_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
  * out_tokens [num_tokens]: rows 0 .. a - 1 the accepted drafts, row a the sampled token, -1 behind
  * it.  emitted[s] = a + 1.  context_next[s] = context_lens[s] - q_s + emitted[s]: the tokens whose
  * K/V rows stay (context_lens count the step's tokens; the next step adds its own); it may be
- * context_lens itself.  A sequence without rows: 0 and context_lens[s].  A row a without a probability
- * above 2^-55: -1 there, emitted[s] = a, PA_DEVERR_BAD_PROBS.  context_lens[s] < q_s: 0, context_lens[s],
- * PA_DEVERR_BAD_CONTEXT.  V <= 2^20; out_tokens must not be tokens.  The launch lets none after it
+ * context_lens itself, but not overlap it otherwise.  A sequence without rows: 0 and context_lens[s].
+ * A row a without a probability above 2^-55: -1 there, emitted[s] = a, PA_DEVERR_BAD_PROBS.  An impossible
+ * span or context_lens[s] < q_s: 0, context_lens[s], PA_DEVERR_BAD_CONTEXT.  V <= 2^20; out_tokens
+ * must not overlap tokens.  The launch lets none after it
  * start early, so the lengths it writes may be read by any call that follows it in the stream.
  * Blocks that a rejected draft had opened stay in the request's table (every call reads
  * ceil(ctx / B) entries); pa_pool_truncate gives them back to the host pool.

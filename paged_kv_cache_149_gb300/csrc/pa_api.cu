@@ -609,6 +609,11 @@ bool rotary_shape_ok(int rotary_dim, float amplitude, int num_seqs, int num_toke
          num_kv_heads <= 65536 && (head_dim == 64 || head_dim == 128) && rotary_dim >= 16 && rotary_dim <= head_dim &&
          rotary_dim % 16 == 0 && std::isfinite(amplitude) && (dtype == PA_FP16 || dtype == PA_BF16);
 }
+// Two arrays of n int32 share memory.
+bool overlap(const int32_t* a, const int32_t* b, int n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return n > 0 && (x < y ? y - x : x - y) < sizeof(int32_t) * static_cast<uintptr_t>(n);
+}
 // Rows of `heads` heads of 16-bit values, `stride` values apart, in 16-byte pieces.
 bool rows_ok(const void* base, int64_t stride, int heads, int head_dim) {
   return base && aligned16(base) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * head_dim;
@@ -760,10 +765,12 @@ int pa_verify_drafts(const int32_t* tokens, const void* target_probs, int64_t ta
     return PA_ERR_ARG;
   if (num_seqs == 0) return PA_OK;
   if (!query_start || !context_lens || !emitted || !context_next) return PA_ERR_ARG;
+  // (each sequence's length is read before its next one is written, others' may not be)
+  if (context_next != context_lens && overlap(context_next, context_lens, num_seqs)) return PA_ERR_ARG;
   const uintptr_t size = dtype == PA_FP32 ? 4 : 2;
   if (num_tokens > 0 &&
       (!tokens || !target_probs || !uniforms || !out_tokens || target_stride < vocab_size ||
-       reinterpret_cast<uintptr_t>(target_probs) % size != 0 || out_tokens == tokens ||
+       reinterpret_cast<uintptr_t>(target_probs) % size != 0 || overlap(out_tokens, tokens, num_tokens) ||
        (draft_probs && (draft_stride < vocab_size || reinterpret_cast<uintptr_t>(draft_probs) % size != 0))))
     return PA_ERR_ARG;
   DeviceInfo di;
