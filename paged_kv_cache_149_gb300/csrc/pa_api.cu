@@ -618,6 +618,10 @@ bool overlap(const int32_t* a, const int32_t* b, int n) {
 bool rows_ok(const void* base, int64_t stride, int heads, int head_dim) {
   return base && aligned16(base) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * head_dim;
 }
+// Rows turned in place keep their places: at another distance one row's output lies over another's input.
+bool in_place_ok(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int rows) {
+  return in != out || in_stride == out_stride || rows <= 1;
+}
 
 }  // namespace
 
@@ -678,7 +682,9 @@ int pa_rotary(const void* q, int64_t q_stride, const void* key, int64_t key_stri
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
   if (!context_lens || !query_start || !freqs || reinterpret_cast<uintptr_t>(freqs) % 8 != 0 ||
       !rows_ok(q, q_stride, num_q_heads, head_dim) || !rows_ok(key, key_stride, num_kv_heads, head_dim) ||
-      !rows_ok(q_out, q_out_stride, num_q_heads, head_dim) || !rows_ok(key_out, key_out_stride, num_kv_heads, head_dim))
+      !rows_ok(q_out, q_out_stride, num_q_heads, head_dim) || !rows_ok(key_out, key_out_stride, num_kv_heads, head_dim) ||
+      !in_place_ok(q, q_stride, q_out, q_out_stride, num_tokens) ||
+      !in_place_ok(key, key_stride, key_out, key_out_stride, num_tokens))
     return PA_ERR_ARG;
   DeviceInfo di;
   if (!device_info(&di)) return PA_ERR_CUDA;
@@ -721,7 +727,8 @@ int pa_rotary_append(const void* q, int64_t q_stride, const void* key, int64_t k
   if (!context_lens || !query_start || !block_tables || !freqs || reinterpret_cast<uintptr_t>(freqs) % 8 != 0 ||
       !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache) ||
       !rows_ok(q, q_stride, num_q_heads, head_dim) || !rows_ok(key, key_stride, num_kv_heads, head_dim) ||
-      !rows_ok(value, value_stride, num_kv_heads, head_dim) || !rows_ok(q_out, q_out_stride, num_q_heads, head_dim))
+      !rows_ok(value, value_stride, num_kv_heads, head_dim) || !rows_ok(q_out, q_out_stride, num_q_heads, head_dim) ||
+      !in_place_ok(q, q_stride, q_out, q_out_stride, num_tokens))
     return PA_ERR_ARG;
   DeviceInfo di;
   if (!device_info(&di)) return PA_ERR_CUDA;
