@@ -57,6 +57,7 @@
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pa_split_plan.h"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
@@ -67,11 +68,6 @@ using namespace tc;
 constexpr int kRows = 128;      // rows of a query tile (MMA M, tensor-memory lanes)
 constexpr int kKeys = 64;       // keys of a K/V tile (MMA N of S, K of P V)
 constexpr int kItems = 4;       // items in flight between the roles
-// An item's start and end, in key tiles, for the shares; and the least key tiles of a piece: a cut that
-// would leave fewer moves to the item's end.  (64 contexts of 128..2048 / 64 rows over 100..1500: 3 and 2
-// 54.9 / 48.6 us, 2 and 4 56.8 / 50.4, 1 and 2 59.5 / 53.9, 4 and 2 55.1 / 49.3.)
-constexpr int kItemCost = 3;
-constexpr int kLeastPiece = 2;
 constexpr int kMaxGrid = 1024;  // CTAs the workspace has descriptors for
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that forces a rescale of O
@@ -444,7 +440,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
     bool wrong = false;
     for (int s = sa; s < sb; ++s) {
       const Seq q = seq_of<CAUSAL>(p, s, per_item);
-      mine += static_cast<long long>(q.blocks) * p.num_kv_heads * (q.tiles + kItemCost);
+      mine += static_cast<long long>(q.blocks) * p.num_kv_heads * item_units(q.tiles);
       wrong = wrong || !q.ok;
     }
     if (wrong && blockIdx.x == 0) atomicOr(p.err, kErrBadContext);
@@ -469,7 +465,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
       total += x;
     }
     const long long at0 = before + incl - mine;
-    const long long grid = gridDim.x, share = max((total + grid - 1) / grid, p.cut ? static_cast<long long>(kLeastPiece) : 1ll);
+    const long long share = share_units(total, gridDim.x, p.cut);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       const long long x = (blockIdx.x + e) * share;
@@ -477,23 +473,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
       long long at = at0;
       for (int s = sa; s < sb; ++s) {
         const Seq q = seq_of<CAUSAL>(p, s, per_item);
-        const long long cost = q.tiles + kItemCost, all = cost * q.blocks * p.num_kv_heads;
+        const long long all = item_units(q.tiles) * q.blocks * p.num_kv_heads;
         if (x < at + all) {
-          long long i = (x - at) / cost;
-          const int off = static_cast<int>((x - at) - i * cost);
-          int tile = max(0, off - kItemCost);
-          const bool whole = !p.cut;
-          if (tile < kLeastPiece && (!whole || off <= 0)) {
-            tile = 0;
-          } else if (whole || q.tiles - tile < kLeastPiece) {  // the item's end, which is the next one's start
-            tile = 0;
-            ++i;
-          }
+          const Place end = place_of(x - at, q.tiles, p.cut);
           int* to = e ? sm.to : sm.from;
           to[0] = s;
-          to[1] = static_cast<int>(i);
-          to[2] = tile;
-          if (e) sm.first_cut = off;
+          to[1] = static_cast<int>(end.item);
+          to[2] = end.tile;
+          if (e) sm.first_cut = end.off;
           break;
         }
         at += all;
@@ -509,8 +496,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) s
         const Seq q = seq_of<CAUSAL>(p, sm.to[0], per_item);
         const bool head = sm.from[0] < sm.to[0] || sm.from[1] < sm.to[1] || sm.from[2] == 0;
         if (head) {
-          // the later cuts of this item lie share units apart
-          j.followers = 1 + static_cast<int>((q.tiles - kLeastPiece + kItemCost - sm.first_cut) / share);
+          j.followers = followers_of(q.tiles, sm.first_cut, share);
           j.s = sm.to[0];
           j.g = sm.to[1] / q.blocks;
           j.qs = q.qs;
