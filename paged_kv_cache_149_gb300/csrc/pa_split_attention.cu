@@ -14,8 +14,10 @@
 // The prefill kernels give each (query tile, sequence, kv head) one SM, which walks all keys:
 // four tokens over 8192 keys with 8 kv heads keep eight SMs busy.  Here the unit of work is 64
 // keys of an item (a sequence, kv head and one or two 128-row query tiles): the batch's units are
-// cut into equal shares, one per SM, wherever the cut falls, so a launch is balanced whatever its
-// lengths are, and only items that a cut goes through are joined, by a second kernel.
+// cut into equal shares, one per SM, wherever the cut falls, so a launch of few rows is balanced whatever
+// its lengths are, and only items that a cut goes through are joined, by a second kernel.  (A causal item
+// counts all keys of its context, although it stops at its last row's: of whole prompts the shares of
+// early rows are short, and pa_prefill is faster.)
 //
 // Design: one CTA per SM (two, of one query tile at head_dim 64); every CTA finds its own share from
 // the lengths (no host round trip, no counter to reset, and the cuts depend on lengths alone: the same bits
@@ -24,7 +26,9 @@
 //   tcgen05 multiplies all 128 rows whatever their number: at 8 kv heads of 128 in bf16 that is
 //   65 K operations per key in the time in which an SM's share of HBM brings the key's 512
 //   bytes, 40 % of the tensor rate, so few rows still stream at the memory's rate; the softmax,
-//   which would not fit, runs in the warps that have rows only.
+//   which would not fit, runs in the warps that have rows only.  Weights enter P V rounded to the
+//   input type, half a step each, since a product's operands have one type and V is not widened; their sum
+//   is of the unrounded ones.
 // * Two loader warps bring 64-key tiles of K and V into a ring, whole blocks by TMA (128-byte
 //   swizzle).  What the last block holds behind the context is masked (K) or cleared in shared memory
 //   (V).  Table entries are looked up 32 blocks at once, a batch ahead.  K's warp also walks the
@@ -42,8 +46,9 @@
 //
 // On GB300, device time: 64 contexts of 128..2048 with up to seven drafts, 32 query / 8 kv heads of
 // 128, bf16, 55 us (285 MB, 5.2 TB/s); eight of 8..32 K with 5..16 rows 96 us (5.9 TB/s); 64 single rows
-// over 100..1500 states, 16 heads of 64, fp16, 49 us; 32 prompts of 3..448 rows over the same 48 us; 6 texts
-// of 900..2048 rows over 2000..8192 states, 32 / 8 heads, 460 us (1530 TFLOP/s).  With few rows a
+// over 100..1500 states, 16 heads of 64, fp16, 49 us; 32 prompts of 3..448 rows over the same 49 us; 6 texts
+// of 900..2048 rows over 2000..8192 states, 32 / 8 heads, 460 us (1530 TFLOP/s) in bursts, 530 call after
+// call (1330), when the power cap holds the SMs near 1.6 GHz.  With few rows a
 // 64-key tile is a chain of fixed latencies (scores read 215 cycles, maximum 250, weights 125, stored and
 // passed on 130, two waits of 100) against 690 (d = 64) or 1380 cycles of an SM's share of HBM: at d = 64
 // that chain bounds the launch, twice over where items are a dozen tiles long and each costs its start
@@ -170,7 +175,9 @@ struct Shape {
   static constexpr int kStages = NT == 2 ? 4 : (D == 128 ? 5 : 4);
 };
 // Two CTAs of 256 threads have 128 registers a thread; the softmax warpgroup takes kSoftmaxRegs, the
-// other keeps kOtherRegs (152 + 104 = 2 x 128).
+// other keeps kOtherRegs (152 + 104 = 2 x 128).  136 to 148 bytes a thread spill all the same (-Xptxas -v), and
+// 6 % of the launch's instructions are loads and stores of them.  (With one CTA an SM nothing spills with one
+// query tile, 8 to 32 bytes with two.)
 constexpr int kSoftmaxRegs = 152;
 constexpr int kOtherRegs = 104;
 
