@@ -1249,7 +1249,8 @@ def decode_drafts(q, k_cache, v_cache, block_tables, context_lens, query_start, 
     """Causal attention of each sequence's newest tokens (rows query_start[s] ..
     query_start[s+1]-1 of q, at positions ctx - q_len .. ctx - 1, their K/V already in the cache)
     over its paged context, the keys of a sequence split over the SMs: for a few tokens a sequence,
-    drafts to be checked say, where prefill would leave most SMs idle.  scale must be positive.
+    drafts to be checked say, where prefill would leave most SMs idle.  (Up to some 256 rows a
+    sequence; whole prompts are prefill's.)  scale must be positive.
     workspace: make_split_workspace.  plan=True returns a Launch instead of launching."""
     return _split_attention("pa_decode_drafts", q, k_cache, v_cache, block_tables, context_lens,
                             query_start, scale, out, workspace, stream, plan)
@@ -1259,8 +1260,9 @@ def decode_drafts(q, k_cache, v_cache, block_tables, context_lens, query_start, 
 def cross(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, out=None,
           workspace=None, stream=None, plan=False):
     """Attention of each sequence's rows of q to all context_lens[s] cached tokens, without a mask:
-    a decoder's tokens over an encoder's states of another length (0 of them: zeros).  Otherwise
-    as decode_drafts."""
+    a decoder's tokens over an encoder's states of another length (0 of them: zeros).  Where every
+    sequence has one row and some states, decode computes the same and is faster.  Otherwise as
+    decode_drafts."""
     return _split_attention("pa_cross", q, k_cache, v_cache, block_tables, context_lens,
                             query_start, scale, out, workspace, stream, plan)
 
